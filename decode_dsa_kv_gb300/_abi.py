@@ -31,6 +31,7 @@ TS_DEVERR_CTX = 0x10
 TS_DEVERR_TIMEOUT = 0x20
 TS_DEVERR_COUNT = 0x40
 TS_DEVERR_ORDER = 0x80
+TS_DEVERR_PROB = 0x100
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -66,6 +67,13 @@ _SIGS = {
                                  _P, _P]),
     "dsa_group_step": (_I, [_P, _P, _P, _P, _P]),
     "dsa_group_step_host": (_I, [_P, _P, _P, _P, _P, _P, _P]),
+    "dsa_cache_row_bytes": (_SZ, [_I]),
+    "dsa_cache_write": (_I, [_P, _I64, _P, _I64, _P, _I, _P, _I64, _I, _P, _P]),
+    "dsa_cache_read": (_I, [_P, _I64, _I, _P, _I64, _I, _P, _P, _I, _I, _P, _P, _P]),
+    "sfa_chunk_workspace_size": (_SZ, [_I, _I, _I]),
+    "sfa_mla_chunk": (_I, [_P, _I64, _P, _I, _I, _I, _P, _I64, _I, _P, _I64, _I, _P, _I, _F, _P, _P,
+                           _P, _SZ, _P, _P]),
+    "ts_verify_drafts": (_I, [_P, _P, _P, _I64, _P, _I64, _P, _I, _I, _I, _P, _P, _P, _P]),
 }
 
 EXPORTS = tuple(_SIGS)
@@ -76,6 +84,8 @@ DSA_POLICY_REUSE = 1
 DSA_POLICY_LRU = 2
 DSA_LAYOUT_SELECTION = 0
 DSA_LAYOUT_STAGED = 1
+DSA_CACHE_BF16 = 0
+DSA_CACHE_E4M3 = 1
 
 
 class DsaGroup(ctypes.Structure):
@@ -297,3 +307,40 @@ def dsa_group_step_host(group: DsaGroup, scores_h, q_h, out_h, scores_d, q_d,
     return _lib.dsa_group_step_host(ctypes.byref(group), ptr(scores_h), ptr(q_h), ptr(out_h),
                                     ptr(scores_d), ptr(q_d),
                                     None if timing is None else ctypes.cast(timing, _P))
+
+
+def dsa_cache_row_bytes(fmt: int) -> int:
+    return int(_lib.dsa_cache_row_bytes(fmt))
+
+
+def dsa_cache_write(latent, latent_stride, rope, rope_stride, slots, n, cache, num_slots, fmt,
+                    err=None, stream=None) -> int:
+    return _lib.dsa_cache_write(ptr(latent), latent_stride, ptr(rope), rope_stride, ptr(slots), n,
+                                ptr(cache), num_slots, fmt, ptr(err), stream_handle(stream))
+
+
+def dsa_cache_read(cache, num_slots, fmt, block_table, table_stride, page_size, pos, ctx_len, B, k,
+                   sel, err=None, stream=None) -> int:
+    return _lib.dsa_cache_read(ptr(cache), num_slots, fmt, ptr(block_table), table_stride,
+                               page_size, ptr(pos), ptr(ctx_len), B, k, ptr(sel), ptr(err),
+                               stream_handle(stream))
+
+
+def sfa_chunk_workspace_size(T: int, B: int, H: int) -> int:
+    return int(_lib.sfa_chunk_workspace_size(T, B, H))
+
+
+def sfa_mla_chunk(q, q_stride, cu_q, T, B, H, cache, num_slots, fmt, block_table, table_stride,
+                  page_size, ctx_len, causal, scale, out, lse, ws, ws_bytes, err=None,
+                  stream=None) -> int:
+    return _lib.sfa_mla_chunk(ptr(q), q_stride, ptr(cu_q), T, B, H, ptr(cache), num_slots, fmt,
+                              ptr(block_table), table_stride, page_size, ptr(ctx_len), int(causal),
+                              float(scale), ptr(out), ptr(lse), ptr(ws), ws_bytes, ptr(err),
+                              stream_handle(stream))
+
+
+def ts_verify_drafts(drafts, n_draft, target, target_stride, draft, draft_stride, u, B, n, V,
+                     tokens, accepted, err=None, stream=None) -> int:
+    return _lib.ts_verify_drafts(ptr(drafts), ptr(n_draft), ptr(target), target_stride, ptr(draft),
+                                 draft_stride, ptr(u), B, n, V, ptr(tokens), ptr(accepted),
+                                 ptr(err), stream_handle(stream))

@@ -460,3 +460,178 @@ class DecodeGroup:
         for ls in self.lstreams:
             ls.synchronize()
         return abi.ts_read_error(self.err, self.main)
+
+
+class PagedKV:
+    """The paged latent cache of one layer (dsa_cache_write, dsa_cache_read,
+    sfa_mla_chunk): num_pages pages of page_size rows, as bf16 or quantised to
+    8 bits (fmt "e4m3"). The caller deals out the pages; a request's position t
+    lies in slot block_table[b][t // page_size] * page_size + t % page_size.
+    `data` are the rows (uint8 [num_pages * page_size][row bytes]), `err` the
+    device error word. Calls enqueue on `stream` (default: the current
+    stream of the cache's device) and do not wait."""
+
+    def __init__(self, num_pages: int, page_size: int = 64, fmt: str = "bf16",
+                 device: str = "cuda"):
+        if fmt not in ("bf16", "e4m3"):
+            raise ValueError(fmt)
+        self.num_pages, self.page_size, self.fmt = num_pages, page_size, fmt
+        self._fmt = abi.DSA_CACHE_BF16 if fmt == "bf16" else abi.DSA_CACHE_E4M3
+        self.num_slots = num_pages * page_size
+        dev = torch.device(device)
+        self.data = torch.zeros((self.num_slots, abi.dsa_cache_row_bytes(self._fmt)),
+                                dtype=torch.uint8, device=dev)
+        self.err = torch.zeros((1,), dtype=torch.int32, device=dev)
+
+    def _int32(self, t: torch.Tensor, name: str, dims: int) -> torch.Tensor:
+        if t.dtype != torch.int32 or t.dim() != dims or t.device != self.data.device:
+            raise ValueError(f"{name}: expected {dims} int32 dimensions on {self.data.device}")
+        if t.numel() and t.stride(-1) != 1:
+            raise ValueError(f"{name}: its last dimension must be contiguous")
+        return t
+
+    def _bf16(self, t: torch.Tensor, name: str, shape) -> torch.Tensor:
+        if (t.dtype not in (torch.bfloat16, torch.int16) or t.device != self.data.device
+                or tuple(t.shape) != tuple(shape)):
+            raise ValueError(f"{name}: expected bf16 {tuple(shape)} on {self.data.device}")
+        return t
+
+    @staticmethod
+    def _stream(stream, device):
+        return torch.cuda.current_stream(device) if stream is None else stream
+
+    def write(self, latent: torch.Tensor, rope: torch.Tensor, slots: torch.Tensor,
+              stream=None) -> None:
+        """Put rows latent [n][512], rope [n][64] (bf16, rows of any stride)
+        into slots [n] (negative: skipped)."""
+        n = latent.shape[0]
+        self._bf16(latent, "latent", (n, DV))
+        self._bf16(rope, "rope", (n, D - DV))
+        if self._int32(slots, "slots", 1).shape[0] != n:
+            raise ValueError("slots: one for each row")
+        if n == 0:
+            return
+        if latent.stride(1) != 1 or rope.stride(1) != 1:
+            raise ValueError("latent, rope: rows must be contiguous")
+        with torch.cuda.device(self.data.device):
+            abi.check(abi.dsa_cache_write(
+                latent, latent.stride(0) if n > 1 else DV, rope,
+                rope.stride(0) if n > 1 else D - DV, slots, n, self.data, self.num_slots,
+                self._fmt, self.err, self._stream(stream, self.data.device)), "dsa_cache_write")
+
+    def read(self, block_table: torch.Tensor, ctx_len: torch.Tensor, pos: torch.Tensor,
+             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The rows of positions pos [B][k] as bf16 [B][k][576]: sfa_mla_decode's
+        selection buffer."""
+        B, k = self._int32(pos, "pos", 2).shape
+        self._table(block_table, ctx_len, B)
+        if not pos.is_contiguous():
+            raise ValueError("pos must be contiguous")
+        st = self._stream(stream, self.data.device)
+        if out is None:
+            with torch.cuda.stream(st):
+                out = torch.empty((B, k, D), dtype=torch.bfloat16, device=self.data.device)
+        if not self._bf16(out, "out", (B, k, D)).is_contiguous():
+            raise ValueError("out must be contiguous")
+        with torch.cuda.device(self.data.device):
+            abi.check(abi.dsa_cache_read(self.data, self.num_slots, self._fmt, block_table,
+                                         self._table_stride(block_table), self.page_size, pos,
+                                         ctx_len, B, k, out, self.err, st), "dsa_cache_read")
+        return out
+
+    def _table(self, block_table, ctx_len, B):
+        self._int32(block_table, "block_table", 2)
+        self._int32(ctx_len, "ctx_len", 1)
+        if block_table.shape[0] != B or ctx_len.shape[0] != B:
+            raise ValueError("block_table, ctx_len: one row for each request")
+        if B > 1 and block_table.stride(0) != block_table.shape[1]:
+            raise ValueError("block_table must be contiguous")
+
+    @staticmethod
+    def _table_stride(block_table):
+        return block_table.shape[1]
+
+    def attend(self, q: torch.Tensor, cu_q: torch.Tensor, block_table: torch.Tensor,
+               ctx_len: torch.Tensor, causal: bool = True, scale: float | None = None,
+               out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               ws: torch.Tensor | None = None, stream=None):
+        """Attention of the newest tokens q [T][H][576] (request b's are rows
+        cu_q[b] .. cu_q[b + 1]) over the cached positions below ctx_len[b];
+        returns (out bf16 [T][H][512], lse float [T][H]). `ws`: a workspace of
+        `workspace(T, B, H)` kept by the caller; without one the call takes its
+        own from PyTorch's allocator, on its stream."""
+        dev = self.data.device
+        T, H = q.shape[0], q.shape[1]
+        B = ctx_len.shape[0]
+        self._bf16(q, "q", (T, H, D))
+        if T and (q.stride(2) != 1 or (H > 1 and q.stride(1) != D)):
+            raise ValueError("q: a token's heads must be contiguous")
+        if self._int32(cu_q, "cu_q", 1).shape[0] != B + 1:
+            raise ValueError("cu_q: one more than the requests")
+        self._table(block_table, ctx_len, B)
+        st = self._stream(stream, dev)
+        with torch.cuda.device(dev), torch.cuda.stream(st):
+            if out is None:
+                out = torch.empty((T, H, DV), dtype=torch.bfloat16, device=dev)
+            if lse is None:
+                lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+            if not self._bf16(out, "out", (T, H, DV)).is_contiguous():
+                raise ValueError("out must be contiguous")
+            if (lse.dtype != torch.float32 or tuple(lse.shape) != (T, H)
+                    or not lse.is_contiguous() or lse.device != dev):
+                raise ValueError(f"lse: expected contiguous float32 {(T, H)} on {dev}")
+            if T == 0:
+                return out, lse
+            if ws is None:
+                ws = self.workspace(T, B, H)
+            abi.check(abi.sfa_mla_chunk(
+                q, q.stride(0) if T > 1 else H * D, cu_q, T, B, H, self.data, self.num_slots,
+                self._fmt, block_table, self._table_stride(block_table), self.page_size, ctx_len,
+                causal, 1.0 / math.sqrt(D) if scale is None else scale, out, lse, ws, ws.numel(),
+                self.err, st), "sfa_mla_chunk")
+        return out, lse
+
+    def workspace(self, T: int, B: int, H: int) -> torch.Tensor:
+        """A workspace of attend for up to T tokens of B requests."""
+        return torch.empty((max(256, abi.sfa_chunk_workspace_size(T, B, H)),), dtype=torch.uint8,
+                           device=self.data.device)
+
+    def synchronize(self, stream=None) -> int:
+        """Wait for the stream and return (and clear) the device error bits."""
+        with torch.cuda.device(self.data.device):
+            return abi.ts_read_error(self.err, self._stream(stream, self.data.device))
+
+
+def verify_drafts(drafts: torch.Tensor, target: torch.Tensor, draft: torch.Tensor | None,
+                  u: torch.Tensor, n_draft: torch.Tensor | None = None,
+                  err: torch.Tensor | None = None, stream=None):
+    """ts_verify_drafts on tensors: drafts int32 [B][n], target float [B][n + 1][V],
+    draft float [B][n][V] or None (certain drafts), u float [B][n + 1], n_draft
+    int32 [B] or None. Returns (tokens int32 [B][n + 1], accepted int32 [B])."""
+    dev = target.device
+    B, n = drafts.shape
+    V = target.shape[2]
+
+    def rows(t, name, count):
+        if t.dtype != torch.float32 or t.device != dev or tuple(t.shape) != (B, count, V):
+            raise ValueError(f"{name}: expected float32 {(B, count, V)} on {dev}")
+        if t.numel() and (t.stride(2) != 1 or (B > 1 and t.stride(0) != count * t.stride(1))):
+            raise ValueError(f"{name}: its rows must be evenly spaced")
+        return t.stride(1)
+
+    ts = rows(target, "target", n + 1)
+    ds = 0 if draft is None else rows(draft, "draft", n)
+    for t, name, dtype, shape in ((drafts, "drafts", torch.int32, (B, n)),
+                                  (u, "u", torch.float32, (B, n + 1)),
+                                  (n_draft, "n_draft", torch.int32, (B,)),
+                                  (err, "err", torch.int32, (1,))):
+        if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or t.device != dev
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name}: expected contiguous {dtype} {shape} on {dev}")
+    st = torch.cuda.current_stream(dev) if stream is None else stream
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        tokens = torch.empty((B, n + 1), dtype=torch.int32, device=dev)
+        accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+        abi.check(abi.ts_verify_drafts(drafts, n_draft, target, max(ts, V), draft, max(ds, V), u,
+                                       B, n, V, tokens, accepted, err, st), "ts_verify_drafts")
+    return tokens, accepted

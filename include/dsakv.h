@@ -63,6 +63,7 @@ typedef enum {
 #define TS_DEVERR_TIMEOUT 0x20    /* a bounded wait inside a kernel gave up */
 #define TS_DEVERR_COUNT 0x40      /* a selection did not come out at size k */
 #define TS_DEVERR_ORDER 0x80      /* ids not strictly ascending where a call needs them so */
+#define TS_DEVERR_PROB 0x100      /* a probability that is NaN, negative or 2 or more, or a row of zeros */
 
 #define TS_D 576        /* values per latent row */
 #define TS_D_LATENT 512 /* latent ("nope") part, also the V part */
@@ -561,6 +562,140 @@ ts_status dsa_group_step(dsa_group* g, const float* scores, const void* q, const
  * All 16-byte aligned. The top-k always runs. Returns as dsa_group_step. */
 ts_status dsa_group_step_host(dsa_group* g, const float* scores_h, const void* q_h, void* out_h,
                               float* scores_d, void* q_d, cudaEvent_t* timing);
+
+/* ---------------------------------------------------------------------------
+ * The paged latent cache: device rows of many requests in pages, written as
+ * tokens arrive, read back by position and attended over by each request's
+ * newest tokens. It serves what the host-offloaded pool does not: prefill
+ * chunks, drafted tokens, layers without an indexer and contexts of at most k
+ * tokens (where the selection is the whole context).
+ *
+ * A cache is num_slots consecutive rows (device memory, 16-byte aligned; for
+ * dsa_cache_read also the device-accessible address of page-locked host
+ * memory). A page is page_size rows; the request's position t lies in slot
+ *   block_table[b * table_stride + t / page_size] * page_size + t % page_size.
+ * Two row formats:
+ *   DSA_CACHE_BF16  1152 bytes: 512 latent + 64 rope values, bf16
+ *   DSA_CACHE_E4M3   656 bytes: 512 e4m3 codes of the latent part, 4 floats,
+ *                    the scale of each 128 codes, then the 64 rope values in
+ *                    bf16 (a position's phase does not stand 3 mantissa bits)
+ * A scale is the smallest power of two s >= 2^-120 with max |x| / s <= 448,
+ * and a code the nearest e4m3 value to x / s (ties to even). A power of two
+ * costs e4m3 nothing but range at its subnormal end, and code * s is then
+ * exact in bf16: what is read back is the stored value itself, and attention
+ * over 8-bit rows equals attention over their bf16 read-back. A NaN stays a
+ * NaN and does not enter the maximum; an infinity comes back as one, its
+ * group's scale being 2^120. (A finite |x| of 2^128 - 2^123 or more rounds up
+ * to an infinity.)
+ * ------------------------------------------------------------------------- */
+#define DSA_CACHE_BF16 0
+#define DSA_CACHE_E4M3 1
+
+/* Bytes of a cache row: 1152, 656, or 0 for an unknown format. */
+size_t dsa_cache_row_bytes(int fmt);
+
+/* dsa_cache_write -- put n new tokens' rows into their slots.
+ *   latent bf16 [n][512], rows latent_stride values apart (>= 512)
+ *   rope   bf16 [n][64],  rows rope_stride values apart (>= 64)
+ *                         both 16-byte aligned, strides multiples of 8; they
+ *                         may be parts of one projection's output
+ *   slots  int32 [n]      the slot of each row; negative: the row is skipped
+ *                         (the padding of a batch). A slot named twice in one
+ *                         call holds an undefined mixture of its rows.
+ * A slot at or past num_slots sets TS_DEVERR_SLOT_RANGE and is skipped. n = 0
+ * enqueues nothing. */
+ts_status dsa_cache_write(const void* latent, int64_t latent_stride, const void* rope,
+                          int64_t rope_stride, const int32_t* slots, int n, void* cache,
+                          int64_t num_slots, int fmt, int32_t* err, cudaStream_t stream);
+
+/* dsa_cache_read -- the rows of selected positions as bf16: sel is then the
+ * selection buffer of sfa_mla_decode (pos = ts_topk's ids gives the sparse
+ * decode over a paged cache).
+ *   block_table int32 [B][table_stride]  page_size a power of two, 16..1024
+ *   pos         int32 [B][k]             in [0, ctx_len[b]), any order
+ *   sel         bf16  [B][k][576]        out, 16-byte aligned
+ * A position outside the context sets TS_DEVERR_ID_RANGE, a page outside the
+ * cache or past the table's row TS_DEVERR_SLOT_RANGE; that row of sel is left
+ * untouched. */
+ts_status dsa_cache_read(const void* cache, int64_t num_slots, int fmt,
+                         const int32_t* block_table, int64_t table_stride, int page_size,
+                         const int32_t* pos, const int32_t* ctx_len, int B, int k, void* sel,
+                         int32_t* err, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * sfa_mla_chunk -- absorbed-MLA attention of each request's newest tokens over
+ * its paged cache (their own rows written before the call). Request b has the
+ * n = cu_q[b + 1] - cu_q[b] query tokens cu_q[b] .. cu_q[b + 1] - 1 and
+ * ctx_len[b] cached positions, the last n of them the query tokens' own. With
+ * causal != 0 token i of the n attends to the positions below
+ *   ctx_len[b] - n + i + 1,
+ * with causal = 0 to all ctx_len[b]. For head h of a token, over its rows K_j:
+ *   s_j = scale * q . K_j ;  p = softmax(s) ;
+ *   out = sum_j p_j K_j[0:512] ;  lse = log(sum_j exp(s_j))
+ * A token that attends to nothing (ctx_len[b] = 0, or more new tokens than
+ * cached positions) has out = 0 and lse = -infinity.
+ *
+ *   q     bf16 [T][H][576]  16-byte aligned, tokens q_stride values apart
+ *                           (>= H * 576, a multiple of 8)
+ *   cu_q  int32 [B + 1]     ascending, cu_q[B] <= T; rows of out and lse that
+ *                           no request has are left as they were. A request
+ *                           may have no token.
+ *   out   bf16 [T][H][512]  16-byte aligned
+ *   lse   float [T][H] or NULL
+ *   ws    workspace of sfa_chunk_workspace_size(T, B, H) bytes, 256-byte
+ *         aligned, contents need not be preserved; calls whose work may
+ *         overlap on the GPU (two streams, two captured graphs) need one each
+ * H <= 1024, T * H < 2^31 - 128, page_size a power of two in 16..1024. Cached
+ * values below ctx_len must be finite (a NaN or an infinity there reaches the
+ * outputs of every token of its tile); rows past ctx_len may hold anything.
+ * bf16 products with fp32 accumulation, softmax statistics in fp32, the
+ * softmax weights rounded to bf16 for the second product. T = 0 enqueues
+ * nothing. cu_q out of order or past T sets TS_DEVERR_ORDER (taken as the
+ * nearest valid value); a ctx_len below 0 or past table_stride * page_size
+ * sets TS_DEVERR_CTX (taken as the nearest valid value); a page outside the
+ * cache sets TS_DEVERR_SLOT_RANGE (the request's output is then undefined);
+ * a wait that gave up sets TS_DEVERR_TIMEOUT.
+ * ------------------------------------------------------------------------- */
+size_t sfa_chunk_workspace_size(int T, int B, int H);
+ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_t* cu_q, int T, int B, int H,
+                        const void* cache, int64_t num_slots, int fmt,
+                        const int32_t* block_table, int64_t table_stride, int page_size,
+                        const int32_t* ctx_len, int causal, float scale, void* out, float* lse,
+                        void* ws, size_t ws_bytes, int32_t* err, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * ts_verify_drafts -- speculative decoding's acceptance: drafted tokens
+ * against the target's probabilities, from given uniform numbers, such that
+ * the tokens that come out are distributed as the target's own. Request b,
+ * with n_draft[b] drafts x_0, x_1, .. (n of them when n_draft is NULL):
+ *   x_i is accepted when x_0 .. x_{i-1} are and u_i * q_i(x_i) < p_i(x_i);
+ *   a = the number of accepted drafts;
+ *   w_t = p_a(t) when every draft was accepted, else max(p_a(t) - q_a(t), 0)
+ *         (p_a(t) when that is zero for every t);
+ *   the next token is the smallest t with w_0 + .. + w_t > u_n * sum w.
+ * The weights are summed as 64-bit multiples of 2^-60, so the result does not
+ * depend on any order of summation.
+ *
+ *   drafts   int32 [B][n]        an id outside [0, V) sets TS_DEVERR_ID_RANGE
+ *                                and counts as refused
+ *   n_draft  int32 [B] or NULL   in [0, n]
+ *   target   float [B][n + 1][V] probabilities after each prefix, rows
+ *                                target_stride floats apart (>= V)
+ *   draft    float [B][n][V]     the draft model's, rows draft_stride apart;
+ *                                NULL: each draft was certain (q one-hot)
+ *   u        float [B][n + 1]    in [0, 1); u[b][n] picks the next token
+ *   tokens   int32 [B][n + 1]    out: the a accepted drafts, the next token,
+ *                                -1 in the places after it
+ *   accepted int32 [B]           out: a
+ * A row's probabilities lie in [0, 2) and add up to less than 16; one that is
+ * NaN, negative or 2 or more counts as 0 and sets TS_DEVERR_PROB, and so does
+ * a row without weight (its next token is -1). n >= 0, V < 2^26; B = 0
+ * enqueues nothing.
+ * ------------------------------------------------------------------------- */
+ts_status ts_verify_drafts(const int32_t* drafts, const int32_t* n_draft, const float* target,
+                           int64_t target_stride, const float* draft, int64_t draft_stride,
+                           const float* u, int B, int n, int V, int32_t* tokens,
+                           int32_t* accepted, int32_t* err, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
