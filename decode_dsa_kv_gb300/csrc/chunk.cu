@@ -1,7 +1,26 @@
 // sfa_mla_chunk: absorbed-MLA attention of each request's newest tokens over
-// its paged latent cache. One CTA per (token, 8 heads), a warp a head: 32 keys
-// at a time go to shared memory as bf16, lane j takes key j's score, and every
-// lane then adds the weighted rows into its 16 of the 512 output dims.
+// its paged latent cache.
+//
+// A request's n x H query rows (token-major: one latent row is every head's
+// key and value, so heads and tokens fold into one long row axis) are cut into
+// tiles of 128 rows, the cached positions into tiles of 256 keys. A pair of
+// CTAs (cta_group::2) takes a row tile over a range of key tiles:
+//   S[128 x 256] = Q[128 x 576] K[256 x 576]^T    36 products of K = 16
+//   O[128 x 512] += P[128 x 256] V[256 x 512]     32 products, N = 256 each
+// Why a pair: O for 128 rows in fp32 is all of one SM's tensor memory (512
+// columns) and leaves none for S. With M = 128 over two CTAs each holds 64
+// rows, its O in 256 columns (lanes 0-63 dims 0-255, lanes 64-127 dims
+// 256-511 of the same rows) and two S buffers in the other 256, so the scores
+// of the next tile are computed while the softmax of this one runs. N = 256 is
+// what the pair needs for its full rate (a product of M = 128 takes 64 clocks
+// at N = 128 and at N = 256, measured).
+//
+// Work is split evenly whatever the lengths: the units (row tile, key tile) of
+// all requests form one line, and each of the SMs' pairs takes an equal
+// stretch of it. A row tile cut by a stretch's end leaves partial sums in the
+// workspace, which chunk_merge_kernel joins in order (no atomics: results do
+// not depend on timing).
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -10,126 +29,980 @@
 namespace dsakv {
 namespace {
 
-constexpr int kKeys = 32;
-constexpr int kHeadsCta = 8;
-constexpr int kThreads = kHeadsCta * 32;
-constexpr int kPitch = DSA_D + 8;  // bf16 values of a key's row in shared memory
+constexpr int kRows = 128;     // query rows of a pair's tile
+constexpr int kRowsCta = 64;   // the rows each CTA of the pair holds
+constexpr int kKeys = 256;     // keys of a tile
+constexpr int kBlocks = 9;     // 64-wide blocks of the 576 dims
+constexpr int kStages = 7;
+constexpr uint32_t kQBlock = kRowsCta * 128;     // 64 rows x 64 dims
+constexpr uint32_t kQBytes = kBlocks * kQBlock;  // 72 KB, resident for a row tile
+constexpr uint32_t kPBlock = kRowsCta * 128;     // 64 rows x 64 keys
+constexpr uint32_t kPBytes = 4 * kPBlock;        // 64 rows x 256 keys
+constexpr uint32_t kStageBytes = 16384;  // K: 128 keys x 64 dims; V: 64 keys x 2 x 64 dims
+constexpr uint32_t kVBox = 64 * 128;     // V: 64 keys x 64 dims
+constexpr uint32_t kBarBytes = 3072;
+constexpr uint32_t kSmemBytes = kBarBytes + 1024 + kQBytes + kPBytes + kStages * kStageBytes;
+static_assert(kSmemBytes <= 227 * 1024, "dynamic shared memory of one CTA");
+constexpr int kSoftmaxWarps = 8;  // warps 0..7: two threads per TMEM lane
+// Loader warps, then one warp that issues the products. bf16 rows come by TMA
+// (three warps, every third stage each); 8-bit rows are converted on their way
+// (seven warps).
+__host__ __device__ constexpr int loader_warps(int fmt) { return fmt == DSA_CACHE_BF16 ? 3 : 7; }
+__host__ __device__ constexpr int threads_of(int fmt) {
+  return 32 * (kSoftmaxWarps + loader_warps(fmt) + 1);
+}
+// Registers a thread after the split: the softmax's two warpgroups take what
+// the others give back (384 x 168 and 512 x 128 at launch).
+__host__ __device__ constexpr int softmax_regs(int fmt) { return fmt == DSA_CACHE_BF16 ? 208 : 152; }
+__host__ __device__ constexpr int other_regs(int fmt) { return fmt == DSA_CACHE_BF16 ? 88 : 104; }
+static_assert(256 * softmax_regs(DSA_CACHE_BF16) + 128 * other_regs(DSA_CACHE_BF16) <= 384 * 168, "");
+static_assert(256 * softmax_regs(DSA_CACHE_E4M3) + 256 * other_regs(DSA_CACHE_E4M3) <= 512 * 128, "");
+constexpr int kMaxPairs = 80;
+constexpr uint32_t kOCol = 256;  // TMEM columns: S buffers 0..127 and 128..255, O 256..511
+constexpr uint64_t kWaitLimit = 2000000000ull;  // 2 s of global timer per wait
+constexpr uint64_t kDrainNs = 2000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// The running maximum follows only when a tile's exceeds it by this much (in
+// powers of two): weights then stay below 2^8, which costs bf16 and the fp32
+// sums no precision, and O is seldom rescaled.
+constexpr float kSlack = 8.f;
+
+struct Bars {
+  uint64_t full[kStages];   // even CTA: a stage's parts in both CTAs have landed
+  uint64_t empty[kStages];  // both: the products reading the stage are done
+  uint64_t q_full;          // even CTA: Q of the row tile in both CTAs
+  uint64_t q_empty;         // both: the row tile's last score product is done
+  uint64_t s_full[2];       // both: a tile's scores are complete
+  uint64_t p_full;          // even CTA: P written and S read in both CTAs
+  uint64_t pv_done;         // both: a tile's value products are complete
+  uint64_t drain;
+  uint64_t sum[16];
+  uint32_t tmem_slot;
+  int abort;
+  int start_b, start_j, start_u;  // where the pair's stretch of work begins
+  int64_t count;                  // and its length in units
+  float red[2][2][kRows];         // exchange between a row's four threads
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
+
+struct Args {
+  const uint8_t* q;
+  int64_t q_stride;  // bytes between tokens
+  const int32_t* cu_q;
+  int T, B, H;
+  const uint8_t* cache;
+  int64_t pages;
+  const int32_t* block_table;
+  int64_t table_stride;
+  int page_shift;
+  const int32_t* ctx_len;
+  int causal;
+  float scale_log2;  // |scale| log2(e)
+  bool negate;       // scale < 0
+  __nv_bfloat16* out;
+  float* lse;
+  int4* meta;    // [pairs][2]: {first output row, rows, flags, 0} of a pair's partial row tiles
+  float2* ml;    // [pairs][2][part_rows]: running maximum (log2) and sum
+  float* opart;  // [pairs][2][part_rows][512]
+  int part_rows;
+  int pairs;
+  uint64_t wait_ns;
+  int32_t* err;
+};
+constexpr uint32_t kIdescNegateA = 1u << 13;
+constexpr int kStarts = 1, kEnds = 2;  // meta flags: holds the row tile's first / last keys
+
+// One request, its values brought into range.
+struct Request {
+  int q0, n, ctx;
+};
+__device__ __forceinline__ Request request(const Args& a, int b) {
+  Request r;
+  r.q0 = min(max(__ldg(a.cu_q + b), 0), a.T);
+  r.n = max(min(__ldg(a.cu_q + b + 1), a.T) - r.q0, 0);
+  const int64_t most = min(a.table_stride << a.page_shift, int64_t(1) << 30);
+  r.ctx = static_cast<int>(min(int64_t(max(__ldg(a.ctx_len + b), 0)), most));
+  return r;
+}
+__device__ __forceinline__ int row_tiles(const Args& a, const Request& r) {
+  return static_cast<int>((int64_t(r.n) * a.H + kRows - 1) / kRows);
+}
+// Keys that the last row of row tile j attends to.
+__device__ __forceinline__ int key_end(const Args& a, const Request& r, int j) {
+  if (!a.causal) return r.ctx;
+  const int64_t last = min(int64_t(r.n) * a.H - 1, int64_t(j) * kRows + kRows - 1);
+  return max(0, r.ctx - r.n + static_cast<int>(last / a.H) + 1);
+}
+__device__ __forceinline__ int key_tiles(int end) { return max(1, (end + kKeys - 1) / kKeys); }
+// Units (key tiles) of a request's first j row tiles, in closed form: row tile
+// i before the last ends with token (128 i + 127) / H, so it has
+//   1 + max(0, floor((ctx - n + (128 i + 127) / H) / 256))
+//     = 1 + max(0, floor((i + c) / 2H)),  c = floor(((ctx - n) H + 127) / 128)
+// key tiles (nested floors of quotients fold into one).
+__device__ __forceinline__ int64_t units_before(const Args& a, const Request& r, int tiles,
+                                                int j) {
+  if (!a.causal) return int64_t(j) * key_tiles(r.ctx);
+  const int64_t G = 2 * int64_t(a.H), c = (int64_t(r.ctx - r.n) * a.H + kRows - 1) >> 7;
+  auto below = [&](int64_t N) -> int64_t {  // sum of floor(i / G) over 0 <= i < N
+    if (N <= 0) return 0;
+    const int64_t k = N / G;
+    return G * (k * (k - 1) / 2) + k * (N - k * G);
+  };
+  const int m = min(j, tiles - 1);
+  int64_t s = m + below(m + c) - below(c);
+  if (j == tiles) s += key_tiles(key_end(a, r, tiles - 1));
+  return s;
+}
+
+// The pair's stretch of the line of all units: thread-per-request sums, then
+// the request, row tile and key tile that the stretch begins in.
+__device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto units_of = [&](int b) -> int64_t {
+    const Request r = request(a, b);
+    return r.n ? units_before(a, r, row_tiles(a, r), row_tiles(a, r)) : 0;
+  };
+  auto warp_scan = [&](int64_t v) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += o;
+    }
+    return v;
+  };
+  int64_t mine = 0;
+  for (int b = tid; b < a.B; b += int(blockDim.x)) mine += units_of(b);
+  mine = warp_scan(mine);
+  if (lane == 31) bars->sum[warp] = mine;
+  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w < (int(blockDim.x) >> 5); ++w) total += bars->sum[w];
+  __syncthreads();
+  const int64_t pairs = min(int64_t(a.pairs), total);
+  const int64_t from = pair < pairs ? total * pair / pairs : 0;
+  const int64_t count = pair < pairs ? total * (pair + 1) / pairs - from : 0;
+  if (tid == 0) bars->count = count;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.B && base <= from && count; b0 += int(blockDim.x)) {
+    const int b = b0 + tid;
+    const int64_t u = b < a.B ? units_of(b) : 0;
+    const int64_t inc = warp_scan(u);
+    if (lane == 31) bars->sum[warp] = inc;
+    __syncthreads();
+    int64_t before = base + inc - u, all = 0;
+    for (int w = 0; w < (int(blockDim.x) >> 5); ++w) {
+      if (w < warp) before += bars->sum[w];
+      all += bars->sum[w];
+    }
+    if (u && from >= before && from < before + u) {
+      const Request r = request(a, b);
+      const int tiles = row_tiles(a, r);
+      int lo = 0, hi = tiles - 1;  // the last row tile that begins at or before `from`
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (units_before(a, r, tiles, mid) <= from - before) lo = mid;
+        else hi = mid - 1;
+      }
+      bars->start_b = b;
+      bars->start_j = lo;
+      bars->start_u = static_cast<int>(from - before - units_before(a, r, tiles, lo));
+    }
+    base += all;
+    __syncthreads();
+  }
+  __syncthreads();
+}
+
+// Reports lengths out of range (once per launch).
+__device__ __forceinline__ void check_lengths(const Args& a) {
+  const int64_t most = min(a.table_stride << a.page_shift, int64_t(1) << 30);
+  for (int b = threadIdx.x; b < a.B; b += int(blockDim.x)) {
+    const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1), ctx = __ldg(a.ctx_len + b);
+    if (c0 < 0 || c1 < c0 || c1 > a.T) report(a.err, TS_DEVERR_ORDER);
+    if (ctx < 0 || ctx > most) report(a.err, TS_DEVERR_CTX);
+  }
+}
+
+// A row tile over a range of its key tiles.
+struct Segment {
+  int b, row0;     // request; first row of the tile within the request's n x H
+  Request r;
+  int rows;        // rows of the tile
+  int t0, t1;      // key tiles
+  int end;         // keys the tile's last row attends to
+  bool starts, ends;
+};
+// Walks the segments of a pair's stretch; every role of both CTAs walks alike.
+struct Walk {
+  int b, j, u;
+  int64_t left;
+  __device__ __forceinline__ Walk(const Bars* bars)
+      : b(bars->start_b), j(bars->start_j), u(bars->start_u), left(bars->count) {}
+  __device__ __forceinline__ bool next(const Args& a, Segment& s) {
+    if (left <= 0) return false;
+    int tiles;
+    for (;; ++b, j = 0) {
+      if (b >= a.B) return false;
+      s.r = request(a, b);
+      tiles = row_tiles(a, s.r);
+      if (j < tiles) break;
+    }
+    s.b = b;
+    s.row0 = j * kRows;
+    s.rows = static_cast<int>(min(int64_t(kRows), int64_t(s.r.n) * a.H - s.row0));
+    s.end = key_end(a, s.r, j);
+    const int units = key_tiles(s.end);
+    s.t0 = u;
+    s.t1 = static_cast<int>(min(int64_t(units), u + left));
+    s.starts = u == 0;
+    s.ends = s.t1 == units;
+    left -= s.t1 - s.t0;
+    if (s.ends) u = 0, ++j;
+    else u = s.t1;
+    return true;
+  }
+};
+
+// 64-key groups of key tile t that hold keys below `end`.
+__device__ __forceinline__ int groups(int end, int t) {
+  return min(4, max(0, (end - t * kKeys + 63) >> 6));
+}
+
+// 2^x on the special-function unit (relative error far below the bf16
+// rounding the weights then get).
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+
+// Barrier of the softmax warps (named barrier 1).
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftmaxWarps) : "memory");
+}
+
+// The same, and whether `ok` holds in every thread of them.
+__device__ __forceinline__ bool softmax_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, r;\n setp.ne.u32 p, %1, 0;\n"
+      " barrier.cta.red.and.pred r, 1, %2, p;\n selp.u32 %0, 1, 0, r;\n}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u), "n"(32 * kSoftmaxWarps)
+      : "memory");
+  return all != 0;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// `bytes` of global memory (16-byte aligned, a multiple of 16) into L2.
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+// 16 e4m3 codes as bf16 values times 2^-120, each four in the order 0, 2, 1, 3
+// (the scale's product brings the 2^120 back). A code's sign, exponent and
+// mantissa bits are moved into a bf16's places; a subnormal code becomes a
+// bf16 subnormal of the same value, so no code is special but NaN (which the
+// cache may not hold below ctx_len). The order costs nothing: Q's latent part
+// is laid out alike, and the epilogue names the output's registers alike.
+__device__ __forceinline__ void widen_codes(const uint4& c, __nv_bfloat162 (&o)[8]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t even = ((w[i] << 8) & 0x80008000u) | ((w[i] << 4) & 0x07f007f0u);
+    const uint32_t odd = (w[i] & 0x80008000u) | ((w[i] >> 4) & 0x07f007f0u);
+    o[2 * i] = *reinterpret_cast<const __nv_bfloat162*>(&even);
+    o[2 * i + 1] = *reinterpret_cast<const __nv_bfloat162*>(&odd);
+  }
+}
+
+// O's dims from the order of widen_codes back to their own.
+template <int kFmt>
+__device__ __forceinline__ void natural_order(uint32_t (&v)[32]) {
+  if (kFmt != DSA_CACHE_E4M3) return;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const uint32_t x = v[i + 1];
+    v[i + 1] = v[i + 2];
+    v[i + 2] = x;
+  }
+}
 
 template <int kFmt>
-__global__ void __launch_bounds__(kThreads)
-    chunk_kernel(const __nv_bfloat16* __restrict__ q, int64_t q_stride,
-                 const int32_t* __restrict__ cu_q, int T, int B, int H,
-                 const uint8_t* __restrict__ cache, int64_t num_slots,
-                 const int32_t* __restrict__ block_table, int64_t table_stride, int page_shift,
-                 const int32_t* __restrict__ ctx_len, int causal, float scale_log2,
-                 __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int32_t* err) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  __nv_bfloat16* ks = reinterpret_cast<__nv_bfloat16*>(smem);
-  float* qs = reinterpret_cast<float*>(smem + kKeys * kPitch * 2);
-  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y * kHeadsCta + warp;
-  if (t == 0 && blockIdx.y == 0)
-    for (int i = threadIdx.x; i <= B; i += kThreads)
-      if (__ldg(cu_q + i) > T || __ldg(cu_q + i) < (i ? __ldg(cu_q + i - 1) : 0))
-        report(err, TS_DEVERR_ORDER);
-  // the request of token t: the last with a start at or before t
-  int lo = 0, hi = B;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu_q + mid) <= t) lo = mid;
-    else hi = mid - 1;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFmt), 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const Args a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Bars* bars = reinterpret_cast<Bars*>(smem_raw);
+  uint8_t* q_tile = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + kBarBytes + 1023) & ~uintptr_t(1023));
+  uint8_t* p_tile = q_tile + kQBytes;
+  uint8_t* ring = p_tile + kPBytes;
+  constexpr int kLoaders = loader_warps(kFmt), kMmaWarp = kSoftmaxWarps + kLoaders;
+  constexpr int kRowBytes = cache_row_bytes(kFmt);
+  volatile int* abort = &bars->abort;
+  const int pair = blockIdx.x >> 1;
+  const uint32_t rank = cluster_ctarank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t wait_ns = a.wait_ns;
+
+  launch_dependents();
+  if (blockIdx.x == 0) check_lengths(a);
+  plan(a, bars, pair);
+  if (bars->count == 0) {  // the same in both CTAs
+    if (rank == 0 && threadIdx.x < 2) a.meta[pair * 2 + threadIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
   }
-  if (lo == B || t < __ldg(cu_q)) return;
-  const int b = lo, first = __ldg(cu_q + b), n = min(__ldg(cu_q + b + 1), T) - first;
-  int ctx = __ldg(ctx_len + b);
-  const int64_t most = min(table_stride << page_shift, int64_t(INT_MAX));
-  if (ctx < 0 || ctx > most) {
-    if (threadIdx.x == 0) report(err, TS_DEVERR_CTX);
-    ctx = ctx < 0 ? 0 : static_cast<int>(most);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars->full[s], 2);
+      mbar_init(&bars->empty[s], 1);
+    }
+    mbar_init(&bars->q_full, 2 * kLoaders);
+    mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->s_full[0], 1);
+    mbar_init(&bars->s_full[1], 1);
+    mbar_init(&bars->p_full, 2 * kSoftmaxWarps);
+    mbar_init(&bars->pv_done, 1);
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    mbar_fence_init();
   }
-  const int limit = causal ? max(0, ctx - n + (t - first) + 1) : ctx;
-  if (h < H)
-    for (int d = lane; d < DSA_D; d += 32)
-      qs[warp * DSA_D + d] = __bfloat162float(q[int64_t(t) * q_stride + int64_t(h) * DSA_D + d]);
-  float m = -INFINITY, l = 0.f, acc[16];
+  if (warp == kMmaWarp) {
+    tmem_alloc_pair(&bars->tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_slot;
+
+  Walk walk(bars);
+  Segment sg;
+  if (warp < kSoftmaxWarps) {
+    // ---------------- softmax and epilogue: two threads per TMEM lane ----------------
+    // Lanes r and r + 64 hold row r: of S keys 0..127 and 128..255, of O dims
+    // 0..255 and 256..511; of either, a lane's two threads take half the columns.
+    regs_inc<softmax_regs(kFmt)>();
+    const int L = (warp & 3) * 32 + lane, r = L & 63, half = L >> 6, part = warp >> 2;
+    const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t p_full = dsmem_addr(&bars->p_full, 0);
+    if (rank == 0 && threadIdx.x == 0)
+      a.meta[pair * 2] = a.meta[pair * 2 + 1] = make_int4(-1, 0, 0, 0);
+    uint32_t tg = 0;  // tiles so far
+    bool ok = true;
+    while (ok && walk.next(a, sg)) {
+      const int rr = rank * kRowsCta + r;  // row within the tile
+      int limit = 0;
+      if (rr < sg.rows)
+        limit = a.causal ? max(0, sg.r.ctx - sg.r.n + (sg.row0 + rr) / a.H + 1) : sg.r.ctx;
+      float m = -INFINITY, l = 0.f;
+      for (int t = sg.t0; t < sg.t1; ++t, ++tg) {
+        const uint32_t ts = trow + (tg & 1) * 128 + part * 64;
+        const int nv = min(max(limit - t * kKeys - half * 128 - part * 64, 0), 64);
+        const bool whole = __all_sync(0xffffffffu, nv == 64);
+        if (ok) ok = mbar_warp_wait<false>(&bars->s_full[tg & 1], (tg >> 1) & 1, abort, wait_ns);
+        // the thread's 64 scores, once, into registers
+        uint32_t x[2][32];
+        float mx = -INFINITY;
+        if (ok) {
+          tc_fence_after();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int k0 = 0; k0 < limit; k0 += kKeys) {
-    __syncthreads();
-    for (int j = warp; j < kKeys; j += kHeadsCta) {
-      const int key = min(k0 + j, limit - 1);
-      const int64_t page = __ldg(block_table + b * table_stride + (key >> page_shift));
-      int64_t slot = (page << page_shift) + (key & ((1 << page_shift) - 1));
-      if (slot < 0 || slot >= num_slots) {
-        if (lane == 0) report(err, TS_DEVERR_SLOT_RANGE);
-        slot = 0;
+          for (int c = 0; c < 2; ++c) tmem_ld32(ts + 32 * c, x[c]);
+          tmem_wait_ld();
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= nv) x[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 64; i += 2)
+            m4[(i >> 1) & 3] =
+                fmaxf(fmaxf(m4[(i >> 1) & 3], __uint_as_float(x[i >> 5][i & 31])),
+                      __uint_as_float(x[i >> 5][(i & 31) + 1]));
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          // (minus infinity times a scale of 0 is no number)
+          mx = mx == -INFINITY ? mx : mx * a.scale_log2;
+        }
+        bars->red[tg & 1][part][L] = mx;
+        softmax_sync();
+        {
+          const auto& e = bars->red[tg & 1];
+          mx = fmaxf(fmaxf(e[0][r], e[1][r]), fmaxf(e[0][r + 64], e[1][r + 64]));
+        }
+        const bool moves = mx > m + kSlack;
+        const float f = moves ? fast_exp2(m - mx) : 1.f;
+        if (moves) m = mx;
+        l *= f;
+        const float mu = m == -INFINITY ? 0.f : m;
+        uint32_t packed[32];
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float p0 = fast_exp2(fmaf(__uint_as_float(x[i >> 4][(2 * i) & 31]), a.scale_log2, -mu));
+          float p1 =
+              fast_exp2(fmaf(__uint_as_float(x[i >> 4][(2 * i + 1) & 31]), a.scale_log2, -mu));
+          if (!whole) {
+            p0 = 2 * i < nv ? p0 : 0.f;
+            p1 = 2 * i + 1 < nv ? p1 : 0.f;
+          }
+          l4[(2 * i) & 3] += p0;
+          l4[(2 * i + 1) & 3] += p1;
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+          packed[i] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        // the tile before this one is in O, and its P read
+        if (ok && tg > 0) ok = mbar_warp_wait<false>(&bars->pv_done, (tg - 1) & 1, abort, wait_ns);
+        if (!ok) continue;  // the barrier above stays matched in every warp
+        if (t > sg.t0 && __any_sync(0xffffffffu, moves)) {
+          tc_fence_after();
+          uint32_t v[32];
+          for (int c = part * 128; c < part * 128 + 128; c += 32) {
+            tmem_ld32(trow + kOCol + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+            tmem_st32(trow + kOCol + c, v);
+          }
+          tmem_wait_st();
+        }
+        uint8_t* prow = p_tile + (half * 2 + part) * kPBlock + r * 128;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(prow + ((j ^ (r & 7)) << 4)) =
+              make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_full);
       }
-      const uint8_t* src = cache + slot * cache_row_bytes(kFmt);
-      uint4* dst = reinterpret_cast<uint4*>(ks + j * kPitch);
-      if (kFmt == DSA_CACHE_BF16) {
-        for (int c = lane; c < DSA_ROW_CHUNKS; c += 32)
-          dst[c] = __ldg(reinterpret_cast<const uint4*>(src) + c);
+      // the row tile's sums: O from TMEM, normalised into the output or raw
+      // into the workspace
+      bars->red[tg & 1][part][L] = l;
+      softmax_sync();
+      {
+        const auto& e = bars->red[tg & 1];
+        l = (e[0][r] + e[1][r]) + (e[0][r + 64] + e[1][r + 64]);
+      }
+      if (ok) ok = mbar_warp_wait<false>(&bars->pv_done, (tg - 1) & 1, abort, wait_ns);
+      ok = softmax_all(ok);  // the same in every warp: all go on, or none
+      if (!ok) break;
+      tc_fence_after();
+      const int64_t grow = int64_t(sg.r.q0) * a.H + sg.row0 + rr;  // output row
+      const bool valid = rr < sg.rows;
+      if (sg.starts && sg.ends) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        uint4* dst = reinterpret_cast<uint4*>(a.out + grow * DSA_DV + half * 256);
+        uint32_t v[32];
+        for (int c = part * 128; c < part * 128 + 128; c += 32) {
+          tmem_ld32(trow + kOCol + c, v);
+          tmem_wait_ld();
+          natural_order<kFmt>(v);
+          if (valid) {
+            uint32_t o[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x0 = l > 0.f ? __uint_as_float(v[2 * i]) * inv : 0.f;
+              const float x1 = l > 0.f ? __uint_as_float(v[2 * i + 1]) * inv : 0.f;
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(x0, x1);
+              o[i] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              dst[c / 8 + j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+        }
+        if (valid && half == 0 && part == 0 && a.lse)
+          a.lse[grow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       } else {
-        uint4 o[2];
-        e4m3x16_to_bf16(__ldg(reinterpret_cast<const uint4*>(src) + lane),
-                        __ldg(reinterpret_cast<const float*>(src + TS_D_LATENT) + (lane >> 3)), o);
-        dst[2 * lane] = o[0];
-        dst[2 * lane + 1] = o[1];
-        if (lane < 8) dst[64 + lane] = __ldg(reinterpret_cast<const uint4*>(src + kE4m3Rope) + lane);
+        const int slot = pair * 2 + (sg.starts ? 1 : 0);
+        const int64_t prow = int64_t(slot) * a.part_rows + rr;
+        float4* dst = reinterpret_cast<float4*>(a.opart + prow * DSA_DV + half * 256);
+        uint32_t v[32];
+        for (int c = part * 128; c < part * 128 + 128; c += 32) {
+          tmem_ld32(trow + kOCol + c, v);
+          tmem_wait_ld();
+          natural_order<kFmt>(v);
+          if (valid) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[c / 4 + j] =
+                  make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                              __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+          }
+        }
+        if (valid && half == 0 && part == 0) a.ml[prow] = make_float2(m, l);
+        if (rank == 0 && threadIdx.x == 0)
+          a.meta[slot] = make_int4(static_cast<int>(int64_t(sg.r.q0) * a.H + sg.row0), sg.rows,
+                                   (sg.starts ? kStarts : 0) | (sg.ends ? kEnds : 0), 0);
       }
+      tc_fence_before();
+    }
+  } else if (warp < kMmaWarp) {
+    // ---------------- loaders: Q, and the K and V stages in turn ----------------
+    regs_dec<other_regs(kFmt)>();
+    const int w = warp - kSoftmaxWarps;
+    const uint32_t q_full = dsmem_addr(&bars->q_full, 0);
+    const uint32_t full0 = dsmem_addr(&bars->full[0], 0);
+    uint32_t s = 0, phase = 1, qn = 0;  // a stage's first use waits for nothing
+    int turn = 0;                       // whose stage is next
+    bool ok = true;
+    const bool el = elect_one();
+    // 16-key steps that one TMA box of a K and of a V stage covers
+    const int k_step = min(8, (1 << a.page_shift) >> 4), v_step = min(4, k_step);
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      if (kFmt == DSA_CACHE_BF16) tma_prefetch_desc(&tm_v);
+    }
+    // the slot of every 16-key step of a segment's key tile: lanes 0..15 (-1:
+    // no such page; keys past the context need none)
+    auto slots_of = [&](const Segment& g, int t) -> int {
+      const int key = t * kKeys + lane * 16;
+      if (lane >= 16 || key >= g.r.ctx || t >= g.t1) return -1;
+      const int64_t page = __ldg(a.block_table + g.b * a.table_stride + (key >> a.page_shift));
+      if (page < 0 || page >= a.pages) {
+        report(a.err, TS_DEVERR_SLOT_RANGE);
+        return -1;
+      }
+      return static_cast<int>((page << a.page_shift) + (key & ((1 << a.page_shift) - 1)));
+    };
+    // this CTA's keys of a tile into L2, page by page: the stages read a row
+    // in nine or more pieces, one stage after another; from L2 they come
+    // sooner, and HBM sees whole pages
+    auto prefetch = [&](int slots) {
+      if (w == 0 && slots >= 0 && lane >> 3 == int(rank) && (lane & (k_step - 1)) == 0)
+        prefetch_l2(a.cache + int64_t(slots) * kRowBytes, k_step * 16 * kRowBytes);
+    };
+    while (ok && walk.next(a, sg)) {
+      int here = -1, now = slots_of(sg, sg.t0), next = slots_of(sg, sg.t0 + 1);
+      prefetch(now);
+      prefetch(next);
+      // Q: rows past the tile's are zeros
+      if (qn > 0) ok = mbar_warp_wait<false>(&bars->q_empty, (qn - 1) & 1, abort, wait_ns);
+      if (!ok) break;
+      for (int i = w; i < kRowsCta; i += kLoaders) {
+        const int rr = rank * kRowsCta + i;
+        const bool valid = rr < sg.rows;
+        const int row = sg.row0 + (valid ? rr : 0);
+        const uint8_t* src = a.q + int64_t(sg.r.q0 + row / a.H) * a.q_stride +
+                             int64_t(row % a.H) * DSA_ROW_BYTES;
+#pragma unroll
+        for (int c0 = 0; c0 < DSA_ROW_CHUNKS; c0 += 32) {
+          const int c = c0 + lane;
+          uint8_t* dst = q_tile + (c >> 3) * kQBlock + i * 128 + (((c & 7) ^ (i & 7)) << 4);
+          if (kFmt == DSA_CACHE_E4M3 && c < 64) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (valid) x = __ldg(reinterpret_cast<const uint4*>(src) + c);
+            *reinterpret_cast<uint4*>(dst) =
+                make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632),
+                           __byte_perm(x.z, x.w, 0x5410), __byte_perm(x.z, x.w, 0x7632));
+          } else if (c < DSA_ROW_CHUNKS) {
+            cp_async16_zfill(dst, src + c * 16, valid);
+          }
+        }
+      }
+      bool q_pending = true;
+      auto q_landed = [&]() {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (el) mbar_arrive_cluster(q_full);
+        q_pending = false;
+      };
+      ++qn;
+
+      // K stage: this CTA's 128 keys of a tile, 64 dims of block kb
+      auto load_k = [&](int kb, uint32_t bytes, uint8_t* dst, uint32_t full) {
+        if (el) mbar_expect_tx_cluster(full, bytes);
+        for (int i = 0; i < 8; i += k_step) {
+          const int slot = __shfl_sync(0xffffffffu, now, rank * 8 + i);
+          if (slot >= 0 && el) tma_load_3d_pair(dst + i * 2048, &tm_k, full, 0, slot, kb);
+        }
+      };
+      // V stage: 64 keys of group g of tile t, dims of blocks kb and kb + 1
+      auto load_v = [&](int t, int g, int kb, uint8_t* dst, uint32_t full) {
+        const int key0 = t * kKeys + g * 64;
+        const bool gaps = __any_sync(0xffffffffu, lane >> 2 == g && here < 0);
+        if (key0 + 64 > sg.r.ctx || gaps) {
+          // V rows that are not the request's must be zeros: their weights
+          // are, but the rows may hold anything, and 0 times NaN is NaN
+          for (int i = 0; i < 32; ++i) {
+            const int row = i * 2 + (lane >> 4), c = lane & 15;  // a row's 16 pieces
+            int slot = __shfl_sync(0xffffffffu, here, g * 4 + (row >> 4));
+            const bool valid = key0 + row < sg.r.ctx && slot >= 0;
+            slot = max(slot, 0) + (valid ? row & 15 : 0);
+            cp_async16_zfill(dst + (c >> 3) * kVBox + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                             a.cache + int64_t(slot) * DSA_ROW_BYTES + kb * 128 + c * 16, valid);
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (el) mbar_arrive_cluster(full);
+          return;
+        }
+        if (el) mbar_expect_tx_cluster(full, kStageBytes);
+        for (int i = 0; i < 4; i += v_step) {
+          const int slot = __shfl_sync(0xffffffffu, here, g * 4 + i);
+          if (el) {
+            tma_load_3d_pair(dst + i * 2048, &tm_v, full, 0, slot, kb);
+            if (v_step < 4) tma_load_3d_pair(dst + kVBox + i * 2048, &tm_v, full, 0, slot, kb + 1);
+          }
+        }
+      };
+      // An 8-bit stage: two halves of 64 keys x 64 dims, half h from the four
+      // 16-key steps of `slots` from step on; keys from `count` on (and those
+      // of bad pages) are zeros. Lane i takes row i / 4 of every eight, and 16
+      // of the 64 codes. The codes are on their way before the stage is free.
+      auto load_codes = [&](int slots, int step0, int step1, int count0, int count1, int kb0,
+                            int kb1, uint8_t* dst, uint32_t full, uint64_t* empty) {
+        const int r0 = lane >> 2, c = lane & 3;
+        uint4 code[2][8];
+        float scale[2][8];
+        auto fetch = [&](const int h) {
+          const int step = h ? step1 : step0, count = h ? count1 : count0, kb = h ? kb1 : kb0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int slot = __shfl_sync(0xffffffffu, slots, step + (i >> 1));
+            code[h][i] = make_uint4(0, 0, 0, 0);
+            scale[h][i] = 1.f;
+            if (slot >= 0 && r0 + 8 * i < count) {
+              const uint8_t* src = a.cache + int64_t(slot + r0 + 8 * (i & 1)) * kE4m3RowBytes;
+              code[h][i] = __ldg(reinterpret_cast<const uint4*>(src + kb * 64) + c);
+              scale[h][i] = __ldg(reinterpret_cast<const float*>(src + TS_D_LATENT) + (kb >> 1));
+            }
+          }
+        };
+        auto store = [&](const int h) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            __nv_bfloat162 o[8];
+            widen_codes(code[h][i], o);
+            // 2^120 scale is past bf16's range for a scale above 2^7
+            const float up = scale[h][i] <= 128.f ? scale[h][i] * 0x1p120f : 0x1p120f;
+            const __nv_bfloat162 f = __float2bfloat162_rn(up);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = __hmul2(o[k], f);
+            if (__any_sync(0xffffffffu, scale[h][i] > 128.f)) {
+              const __nv_bfloat162 f2 =
+                  __float2bfloat162_rn(scale[h][i] <= 128.f ? 1.f : scale[h][i]);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] = __hmul2(o[k], f2);
+            }
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(o);
+            uint8_t* row = dst + h * kVBox + (r0 + 8 * i) * 128;
+            *reinterpret_cast<uint4*>(row + (((2 * c) ^ r0) << 4)) =
+                make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ r0) << 4)) =
+                make_uint4(u[4], u[5], u[6], u[7]);
+          }
+        };
+        fetch(0);
+        ok = mbar_warp_wait<false>(empty, phase, abort, wait_ns);
+        if (!ok) return;
+        fetch(1);
+        store(0);
+        store(1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (el) mbar_arrive_cluster(full);
+      };
+      // the stages in the order the products take them, dealt to the warps in turn
+      for (int t = sg.t0; t <= sg.t1 && ok; ++t) {
+        const bool scores = t < sg.t1;
+        const int ahead = slots_of(sg, t + 2);
+        prefetch(ahead);
+        if (t == sg.t1 - 1 && w == 0) {  // the next segment's first tile
+          Walk peek = walk;
+          Segment g;
+          if (peek.next(a, g)) prefetch(slots_of(g, g.t0));
+        }
+        const uint32_t boxes = __popc(__ballot_sync(
+            0xffffffffu, now >= 0 && lane >> 3 == int(rank) && (lane & (k_step - 1)) == 0));
+        const int n = (scores ? kBlocks : 0) + (t > sg.t0 ? 2 * groups(sg.end, t - 1) : 0);
+        for (int i = 0; i < n && ok; ++i) {
+          if (turn == w) {
+            uint8_t* dst = ring + s * kStageBytes;
+            const uint32_t full = full0 + s * 8;
+            const bool is_k = scores && i < kBlocks;
+            const int v = scores ? i - kBlocks : i;  // V: group v / 2, dims half v % 2
+            const int vb = rank * 4 + (v & 1) * 2;
+            if (kFmt == DSA_CACHE_E4M3 && !(is_k && i == kBlocks - 1)) {
+              if (is_k) {
+                const int left = sg.r.ctx - t * kKeys - int(rank) * 128;
+                load_codes(now, rank * 8, rank * 8 + 4, left, left - 64, i, i, dst, full,
+                           &bars->empty[s]);
+              } else {
+                const int g = v >> 1, left = sg.r.ctx - (t - 1) * kKeys - g * 64;
+                load_codes(here, g * 4, g * 4, left, left, vb, vb + 1, dst, full, &bars->empty[s]);
+              }
+            } else {
+              ok = mbar_warp_wait<false>(&bars->empty[s], phase, abort, wait_ns);
+              if (ok) {
+                // (the 8-bit format's rope part is bf16: its map has one block)
+                if (is_k) load_k(kFmt == DSA_CACHE_E4M3 ? 0 : i, boxes * k_step * 2048, dst, full);
+                else load_v(t - 1, v >> 1, vb, dst, full);
+              }
+            }
+            // Q's copies landed beside this warp's first stage (its second may
+            // wait for products, and they for Q)
+            if (q_pending) q_landed();
+          }
+          if (++turn == kLoaders) turn = 0;
+          if (++s == kStages) s = 0, phase ^= 1;
+        }
+        here = now;
+        now = next;
+        next = ahead;
+      }
+    }
+  } else {
+    regs_dec<other_regs(kFmt)>();
+    if (rank == 0) {
+      // ---------------- MMA issuer (the even CTA's, for both) ----------------
+      // a negative scale negates Q (its bit of the instruction descriptor)
+      const uint32_t id_s =
+          idesc_bf16_f32(kRows, kKeys, false, false) | (a.negate ? kIdescNegateA : 0u);
+      const uint32_t id_pv = idesc_bf16_f32(kRows, 256, false, true);
+      // descriptors of the first 16-wide step; later ones differ in the start
+      // address (16-byte units, no carry out of its field)
+      const uint64_t q_desc = smem_desc_sw128(smem_addr(q_tile), 16, 1024);
+      const uint64_t p_desc = smem_desc_sw128(smem_addr(p_tile), 16, 1024);
+      const uint64_t k_desc = smem_desc_sw128(smem_addr(ring), 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(smem_addr(ring), kVBox, 1024);
+      const bool el = elect_one();
+      uint32_t s = 0, phase = 0, tg = 0, qn = 0;
+      bool ok = true;
+      // the next `count` stages, in both CTAs (the waits of several stages
+      // overlap: a stage's own wait, vote and election cost 220-350 clocks of
+      // this warp, more than the 257 of its four products if taken one by one)
+      auto landed = [&](const int count) -> bool {
+        bool all = true;
+        uint32_t s1 = s, phase1 = phase;
+#pragma unroll
+        for (int i = 0; i < count; ++i) {
+          all &= mbar_try_wait(&bars->full[s1], phase1);
+          if (++s1 == kStages) s1 = 0, phase1 ^= 1;
+        }
+        if (!__all_sync(0xffffffffu, all)) {
+          s1 = s, phase1 = phase;
+          for (int i = 0; i < count && ok; ++i) {
+            ok = mbar_warp_wait<false>(&bars->full[s1], phase1, abort, wait_ns);
+            if (++s1 == kStages) s1 = 0, phase1 ^= 1;
+          }
+        }
+        tc_fence_after();
+        return ok;
+      };
+      auto advance = [&]() {
+        if (++s == kStages) s = 0, phase ^= 1;
+      };
+      while (ok && walk.next(a, sg)) {
+        ok = mbar_warp_wait<true>(&bars->q_full, qn & 1, abort, wait_ns);
+        ++qn;
+        for (int t = sg.t0; t <= sg.t1 && ok; ++t) {
+          if (t < sg.t1) {
+            const uint32_t d = tmem + (tg & 1) * 128;
+#pragma unroll
+            for (int kb = 0; kb < kBlocks; kb += 3) {
+              if (!landed(3)) break;
+#pragma unroll
+              for (int i = 0; i < 3; ++i) {
+                const uint64_t qd = q_desc + (kb + i) * (kQBlock >> 4);
+                const uint64_t kd = k_desc + s * (kStageBytes >> 4);
+                if (el) {
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_bf16_pair(d, qd + kk * 2, kd + kk * 2, id_s, (kb | i | kk) != 0);
+                  tc_commit_pair(&bars->empty[s]);
+                }
+                advance();
+              }
+            }
+            if (!ok) break;
+            if (el) {
+              tc_commit_pair(&bars->s_full[tg & 1]);
+              if (t == sg.t1 - 1) tc_commit_pair(&bars->q_empty);
+            }
+            ++tg;
+          }
+          if (t > sg.t0) {
+            // the tile before: tg counts one more when this one's scores were issued
+            const uint32_t tp = t < sg.t1 ? tg - 2 : tg - 1;
+            ok = mbar_warp_wait<true>(&bars->p_full, tp & 1, abort, wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const int g1 = groups(sg.end, t - 1);
+            const bool first = t - 1 == sg.t0;
+            for (int g = 0; g < g1 && landed(2); ++g) {
+              const uint64_t pd = p_desc + g * (kPBlock >> 4);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint64_t vd = v_desc + s * (kStageBytes >> 4);
+                if (el) {
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_bf16_pair(tmem + kOCol + j * 128, pd + kk * 2, vd + kk * (2048 >> 4),
+                                     id_pv, !first || (g | kk) != 0);
+                  tc_commit_pair(&bars->empty[s]);
+                }
+                advance();
+              }
+            }
+            if (ok && el) tc_commit_pair(&bars->pv_done);
+          }
+        }
+      }
+    }
+  }
+
+  // ---------------- teardown ----------------
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (bars->abort) {
+    if (threadIdx.x == 0) report(a.err, TS_DEVERR_TIMEOUT);
+    // copies in flight land, and every tcgen05 operation issued completes,
+    // before the CTA may leave
+    if (threadIdx.x == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
+    }
+    if (warp == kMmaWarp && rank == 0 && elect_one()) {
+      tc_commit_pair(&bars->drain);
+      mbar_wait_timed(&bars->drain, 0, kWaitLimit);
     }
     __syncthreads();
-    if (h >= H) continue;
-    float s = 0.f;
-    const uint4* kr = reinterpret_cast<const uint4*>(ks + lane * kPitch);
-    for (int c = 0; c < DSA_ROW_CHUNKS; ++c) {
-      const uint4 v = kr[c];
-      const float* qq = qs + warp * DSA_D + c * 8;
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  }
+  cluster_sync_all();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// Joins the partial sums of the row tiles that stretches of work have cut: the
+// head (a pair's segment that holds a row tile's first keys) and the pairs
+// after it up to the segment that holds its last,
+//   out = sum_i w_i O_i / sum_i w_i l_i,  w_i = 2^(m_i - max m).
+// A warp a row; pairs without a head leave at once.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Args a) {
+  wait_previous_kernel();
+  const int pair = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 head = a.meta[pair * 2 + 1];
+  const int r = blockIdx.y * kMergeWarps + warp;
+  if (head.x < 0 || r >= head.y) return;
+  // the segments: slot 1 of this pair, slot 0 of the next ones
+  int parts = 0;
+  for (int p0 = pair + 1; p0 < a.pairs && !parts; p0 += 32) {
+    const int p = p0 + lane;
+    const bool last = p < a.pairs && a.meta[p * 2].x >= 0 && (a.meta[p * 2].z & kEnds);
+    const uint32_t who = __ballot_sync(0xffffffffu, last);
+    if (who) parts = p0 + __ffs(who) - pair;
+  }
+  auto row_of = [&](int i) -> int64_t {
+    return int64_t(i == 0 ? pair * 2 + 1 : (pair + i) * 2) * a.part_rows + r;
+  };
+  constexpr int kPer = (kMaxPairs + 31) / 32;
+  float w[kPer], l[kPer], mx = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s += qq[2 * i] * __uint_as_float(w[i] << 16);
-        s += qq[2 * i + 1] * __uint_as_float(w[i] & 0xffff0000u);
-      }
-    }
-    s = k0 + lane < limit ? s * scale_log2 : -INFINITY;
-    float mx = s;
+  for (int k = 0; k < kPer; ++k) {
+    const int i = lane + 32 * k;
+    const float2 e = i < parts ? a.ml[row_of(i)] : make_float2(-INFINITY, 0.f);
+    w[k] = e.x;
+    l[k] = e.y;
+    mx = fmaxf(mx, e.x);
+  }
 #pragma unroll
-    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    const float mn = fmaxf(m, mx), f = exp2f(m - mn), p = exp2f(s - mn);
-    float ps = p;
+  for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  float sum = 0.f;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, d);
-    m = mn;
-    l = l * f + ps;
+  for (int k = 0; k < kPer; ++k) {
+    w[k] = mx == -INFINITY ? 0.f : exp2f(w[k] - mx);
+    sum += w[k] * l[k];
+  }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] *= f;
-    for (int j = 0; j < kKeys; ++j) {
-      const float pj = __shfl_sync(0xffffffffu, p, j);
-      const uint4* vr = reinterpret_cast<const uint4*>(ks + j * kPitch) + 2 * lane;
-      const uint4 v0 = vr[0], v1 = vr[1];
-      const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  float acc[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[2 * i] += pj * __uint_as_float(w[i] << 16);
-        acc[2 * i + 1] += pj * __uint_as_float(w[i] & 0xffff0000u);
+  for (int c = 0; c < 16; ++c) acc[c] = 0.f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int n = min(parts - 32 * k, 32);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w[k], i);
+      const float4* src =
+          reinterpret_cast<const float4*>(a.opart + row_of(32 * k + i) * DSA_DV) + lane;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 x = __ldcs(src + 32 * c);
+        acc[4 * c] += wi * x.x;
+        acc[4 * c + 1] += wi * x.y;
+        acc[4 * c + 2] += wi * x.z;
+        acc[4 * c + 3] += wi * x.w;
       }
     }
   }
-  if (h >= H) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint32_t o[8];
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int64_t row = int64_t(head.x) + r;
+  uint2* dst = reinterpret_cast<uint2*>(a.out + row * DSA_DV) + lane;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+  for (int c = 0; c < 4; ++c) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[4 * c] * inv, acc[4 * c + 1] * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv);
+    dst[32 * c] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                             *reinterpret_cast<const uint32_t*>(&hi));
   }
-  uint4* dst = reinterpret_cast<uint4*>(out + (int64_t(t) * H + h) * DSA_DV) + 2 * lane;
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-  if (lse && lane == 0) lse[int64_t(t) * H + h] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+  if (lane == 0 && a.lse) a.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+__host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// 3-D map over cache rows of blocks of 64 bf16: dims {64, rows, blocks}; box
+// {64, box_rows, box_blocks}.
+bool make_map(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_bytes,
+              uint64_t blocks, uint32_t box_rows, uint32_t box_blocks) {
+  EncodeTiled enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {64, rows, blocks};
+  const cuuint64_t strides[2] = {row_bytes, 128};
+  const cuuint32_t box[3] = {64, box_rows, box_blocks};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int part_rows(int T, int H) { return static_cast<int>(std::min(int64_t(T) * H, int64_t(kRows))); }
+
+// The attention's launch; the maps and the merge are the caller's.
+template <int kFmt>
+ts_status launch_chunk(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Args& a,
+                       cudaStream_t stream) {
+  static std::atomic<uint64_t> smem_set{0};
+  if (!raise_smem_limit(reinterpret_cast<const void*>(chunk_kernel<kFmt>), kSmemBytes, smem_set))
+    return TS_ERR_CUDA;
+  chunk_kernel<kFmt><<<2 * a.pairs, threads_of(kFmt), kSmemBytes, stream>>>(tm_k, tm_v, a);
+  return launch_status();
 }
 
 }  // namespace
@@ -139,7 +1012,8 @@ using namespace dsakv;
 
 extern "C" size_t sfa_chunk_workspace_size(int T, int B, int H) {
   if (T <= 0 || B <= 0 || H <= 0) return 0;
-  return 256;
+  const size_t slots = 2 * kMaxPairs, rows = slots * part_rows(T, H);
+  return align256(slots * sizeof(int4)) + align256(rows * sizeof(float2)) + rows * DSA_DV * 4;
 }
 
 extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_t* cu_q, int T,
@@ -156,28 +1030,66 @@ extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_
   if (!q || !cu_q || !ctx_len || !out || !ws || !aligned16(q) || !aligned16(out))
     return TS_ERR_INVALID_ARG;
   if (q_stride < int64_t(H) * DSA_D || q_stride % 8 != 0) return TS_ERR_INVALID_ARG;
-  if (H > 1024 || int64_t(T) * H >= INT_MAX - 127) return TS_ERR_UNSUPPORTED;
+  if (H > 1024 || int64_t(T) * H >= INT_MAX - 127 || num_slots > INT_MAX)
+    return TS_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0 ||
       ws_bytes < sfa_chunk_workspace_size(T, B, H))
     return TS_ERR_WORKSPACE;
-  const int smem = kKeys * kPitch * 2 + kHeadsCta * DSA_D * 4;
-  const dim3 grid(T, (H + kHeadsCta - 1) / kHeadsCta);
-  const auto* qb = static_cast<const __nv_bfloat16*>(q);
-  const auto* c = static_cast<const uint8_t*>(cache);
-  auto* o = static_cast<__nv_bfloat16*>(out);
-  const int shift = __builtin_ctz(page_size);
-  static std::atomic<uint64_t> set[2];
-  const void* fn = fmt == DSA_CACHE_BF16
-                       ? reinterpret_cast<const void*>(chunk_kernel<DSA_CACHE_BF16>)
-                       : reinterpret_cast<const void*>(chunk_kernel<DSA_CACHE_E4M3>);
-  if (!raise_smem_limit(fn, smem, set[fmt])) return TS_ERR_CUDA;
-  if (fmt == DSA_CACHE_BF16)
-    chunk_kernel<DSA_CACHE_BF16><<<grid, kThreads, smem, stream>>>(
-        qb, q_stride, cu_q, T, B, H, c, num_slots, block_table, table_stride, shift, ctx_len,
-        causal, scale * kLog2e, o, lse, err);
-  else
-    chunk_kernel<DSA_CACHE_E4M3><<<grid, kThreads, smem, stream>>>(
-        qb, q_stride, cu_q, T, B, H, c, num_slots, block_table, table_stride, shift, ctx_len,
-        causal, scale * kLog2e, o, lse, err);
-  return launch_status();
+  Args a = {};
+  a.q = static_cast<const uint8_t*>(q);
+  a.q_stride = q_stride * 2;
+  a.cu_q = cu_q;
+  a.T = T;
+  a.B = B;
+  a.H = H;
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.pages = num_slots / page_size;
+  a.block_table = block_table;
+  a.table_stride = table_stride;
+  a.page_shift = __builtin_ctz(page_size);
+  a.ctx_len = ctx_len;
+  a.causal = causal;
+  a.scale_log2 = std::fabs(scale) * kLog2e;
+  a.negate = scale < 0.f;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.part_rows = part_rows(T, H);
+  a.pairs = std::max(1, std::min(kMaxPairs, sm_count() / 2));
+  const size_t slots = 2 * kMaxPairs, rows = slots * a.part_rows;
+  char* w = static_cast<char*>(ws);
+  a.meta = reinterpret_cast<int4*>(w);
+  w += align256(slots * sizeof(int4));
+  a.ml = reinterpret_cast<float2*>(w);
+  w += align256(rows * sizeof(float2));
+  a.opart = reinterpret_cast<float*>(w);
+  a.wait_ns = wait_limit_ns(kWaitLimit);
+  a.err = err;
+  CUtensorMap tm_k, tm_v;
+  if (fmt == DSA_CACHE_BF16) {
+    if (!make_map(&tm_k, cache, num_slots, DSA_ROW_BYTES, kBlocks, std::min(page_size, 128), 1) ||
+        !make_map(&tm_v, cache, num_slots, DSA_ROW_BYTES, kBlocks, std::min(page_size, 64),
+                  page_size >= 64 ? 2 : 1))
+      return TS_ERR_CUDA;
+    st = launch_chunk<DSA_CACHE_BF16>(tm_k, tm_v, a, stream);
+  } else {
+    if (!make_map(&tm_k, a.cache + kE4m3Rope, num_slots, kE4m3RowBytes, 1,
+                  std::min(page_size, 128), 1))
+      return TS_ERR_CUDA;
+    st = launch_chunk<DSA_CACHE_E4M3>(tm_k, tm_k, a, stream);
+  }
+  if (st != TS_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.pairs, (a.part_rows + kMergeWarps - 1) / kMergeWarps);
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, chunk_merge_kernel, a) != cudaSuccess) {
+    cudaGetLastError();
+    return TS_ERR_CUDA;
+  }
+  return TS_OK;
 }

@@ -621,27 +621,9 @@ __global__ void __launch_bounds__(kHeads) sfa_combine_kernel(const float* __rest
 
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-  static EncodeTiled fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiled>(p);
-  }
-  return fn;
-}
-
 // 3-D map over rows of 576 bf16: dims {576, rows, batch}; box {64, box_rows, 1}.
 bool make_map(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t batch, uint32_t box_rows) {
-  EncodeTiled enc = encoder();
+  EncodeTiled enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[3] = {DSA_D, rows, batch};
   const cuuint64_t strides[2] = {DSA_ROW_BYTES, rows * DSA_ROW_BYTES};
