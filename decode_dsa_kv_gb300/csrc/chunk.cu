@@ -33,7 +33,6 @@ constexpr int kRows = 128;     // query rows of a pair's tile
 constexpr int kRowsCta = 64;   // the rows each CTA of the pair holds
 constexpr int kKeys = 256;     // keys of a tile
 constexpr int kBlocks = 9;     // 64-wide blocks of the 576 dims
-constexpr int kStages = 7;
 constexpr uint32_t kQBlock = kRowsCta * 128;     // 64 rows x 64 dims
 constexpr uint32_t kQBytes = kBlocks * kQBlock;  // 72 KB, resident for a row tile
 constexpr uint32_t kPBlock = kRowsCta * 128;     // 64 rows x 64 keys
@@ -41,22 +40,31 @@ constexpr uint32_t kPBytes = 4 * kPBlock;        // 64 rows x 256 keys
 constexpr uint32_t kStageBytes = 16384;  // K: 128 keys x 64 dims; V: 64 keys x 2 x 64 dims
 constexpr uint32_t kVBox = 64 * 128;     // V: 64 keys x 64 dims
 constexpr uint32_t kBarBytes = 3072;
-constexpr uint32_t kSmemBytes = kBarBytes + 1024 + kQBytes + kPBytes + kStages * kStageBytes;
-static_assert(kSmemBytes <= 227 * 1024, "dynamic shared memory of one CTA");
 constexpr int kSoftmaxWarps = 8;  // warps 0..7: two threads per TMEM lane
-// Loader warps, then one warp that issues the products. bf16 rows come by TMA
-// (three warps, every third stage each); 8-bit rows are converted on their way
-// (seven warps).
-__host__ __device__ constexpr int loader_warps(int fmt) { return fmt == DSA_CACHE_BF16 ? 3 : 7; }
-__host__ __device__ constexpr int threads_of(int fmt) {
-  return 32 * (kSoftmaxWarps + loader_warps(fmt) + 1);
-}
-// Registers a thread after the split: the softmax's two warpgroups take what
-// the others give back (384 x 168 and 512 x 128 at launch).
-__host__ __device__ constexpr int softmax_regs(int fmt) { return fmt == DSA_CACHE_BF16 ? 208 : 152; }
-__host__ __device__ constexpr int other_regs(int fmt) { return fmt == DSA_CACHE_BF16 ? 88 : 104; }
-static_assert(256 * softmax_regs(DSA_CACHE_BF16) + 128 * other_regs(DSA_CACHE_BF16) <= 384 * 168, "");
-static_assert(256 * softmax_regs(DSA_CACHE_E4M3) + 256 * other_regs(DSA_CACHE_E4M3) <= 512 * 128, "");
+// bf16 rows: warps 8..10 load by TMA (every third stage each), warp 11 issues
+// the products. 8-bit rows: warps 8..13 convert (every sixth stage each, from
+// two halves of a stage's codes that each warp keeps in flight), warp 14 loads
+// Q, warp 15 issues the products.
+constexpr int kTmaWarps = 3, kConvertWarps = 6;
+constexpr uint32_t kRawHalf = 4096;  // 64 keys x 64 codes
+template <int kFmt>
+struct Layout {
+  static constexpr bool k8 = kFmt == DSA_CACHE_E4M3;
+  static constexpr int kLoaders = k8 ? kConvertWarps + 1 : kTmaWarps;
+  static constexpr int kMmaWarp = kSoftmaxWarps + kLoaders;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr int kStages = k8 ? 4 : 7;
+  static constexpr uint32_t kRawBytes = k8 ? 2 * kConvertWarps * kRawHalf : 0;
+  static constexpr uint32_t kSmem =
+      kBarBytes + 1024 + kQBytes + kPBytes + kStages * kStageBytes + kRawBytes;
+  static_assert(kSmem <= 227 * 1024, "dynamic shared memory of one CTA");
+  // Registers a thread after the split: the softmax's two warpgroups take what
+  // the others give back (of 384 x 168, or 512 x 128, at launch).
+  static constexpr int kSoftmaxRegs = k8 ? 152 : 208, kOtherRegs = k8 ? 104 : 88;
+  static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <=
+                    kThreads * (k8 ? 128 : 168), "register split");
+};
+constexpr int kMaxStages = 7;
 constexpr int kMaxPairs = 80;
 constexpr uint32_t kOCol = 256;  // TMEM columns: S buffers 0..127 and 128..255, O 256..511
 constexpr uint64_t kWaitLimit = 2000000000ull;  // 2 s of global timer per wait
@@ -69,13 +77,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;
 
 struct Bars {
-  uint64_t full[kStages];   // even CTA: a stage's parts in both CTAs have landed
-  uint64_t empty[kStages];  // both: the products reading the stage are done
+  uint64_t full[kMaxStages];   // even CTA: a stage's parts in both CTAs have landed
+  // both: the products reading the stage are done; a place's uses alternate
+  // between two barriers
+  uint64_t empty[2][kMaxStages];
   uint64_t q_full;          // even CTA: Q of the row tile in both CTAs
   uint64_t q_empty;         // both: the row tile's last score product is done
   uint64_t s_full[2];       // both: a tile's scores are complete
   uint64_t p_full;          // even CTA: P written and S read in both CTAs
   uint64_t pv_done;         // both: a tile's value products are complete
+  uint64_t raw[kConvertWarps][2];  // a converting warp's half-stages of codes
+  uint64_t q_raw;                  // Q as loaded (8-bit rows: reordered before use)
   uint64_t drain;
   uint64_t sum[16];
   uint32_t tmem_slot;
@@ -89,6 +101,7 @@ static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 struct Args {
   const uint8_t* q;
   int64_t q_stride;  // bytes between tokens
+  bool q_dense;      // the tokens lie side by side: Q by TMA
   const int32_t* cu_q;
   int T, B, H;
   const uint8_t* cache;
@@ -331,30 +344,450 @@ __device__ __forceinline__ void widen_codes(const uint4& c, __nv_bfloat162 (&o)[
   }
 }
 
+// 8 bf16 values, each four in the order of widen_codes.
+__device__ __forceinline__ uint4 code_order(const uint4& x) {
+  return make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632),
+                    __byte_perm(x.z, x.w, 0x5410), __byte_perm(x.z, x.w, 0x7632));
+}
+
 // O's dims from the order of widen_codes back to their own.
 template <int kFmt>
 __device__ __forceinline__ void natural_order(uint32_t (&v)[32]) {
-  if (kFmt != DSA_CACHE_E4M3) return;
+  if (kFmt == DSA_CACHE_E4M3) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const uint32_t x = v[i + 1];
-    v[i + 1] = v[i + 2];
-    v[i + 2] = x;
+    for (int i = 0; i < 32; i += 4) {
+      const uint32_t x = v[i + 1];
+      v[i + 1] = v[i + 2];
+      v[i + 2] = x;
+    }
+  }
+}
+
+struct Maps {
+  CUtensorMap q;     // [T H rows][9 blocks of 64], box 64 rows x 9 blocks
+  CUtensorMap k;     // cache rows, box min(page, 128) rows x 1 block (8-bit rows: the rope part)
+  CUtensorMap v;     // cache rows, box min(page, 64) rows x 2 blocks (1 below 64)
+  CUtensorMap code;  // 8-bit rows: the codes, box min(page, 64) rows x 64
+};
+
+// What the loading warps share.
+struct Loader {
+  const Args& a;
+  const Maps& maps;
+  Bars* bars;
+  uint8_t *q_tile, *ring, *raw;
+  uint32_t rank, q_full, full;  // cluster addresses of the even CTA's barriers
+  int lane;
+  bool el;  // this lane issues
+  volatile int* abort;
+  // 16-key steps that one TMA box of a K stage and of 64 keys covers
+  int k_step, v_step;
+
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    return mbar_warp_wait<false>(bar, parity, abort, a.wait_ns);
+  }
+  // The place of a stage's use number `wrap` is free once the use before is
+  // consumed. Uses alternate between two barriers, so a warp that has not
+  // looked at this place for two uses is still told apart (a barrier's parity
+  // tells two phases): its stages may be up to 2 * kStages apart.
+  __device__ __forceinline__ bool wait_free(uint32_t s, uint32_t wrap) {
+    return wrap == 0 || wait(&bars->empty[(wrap - 1) & 1][s], ((wrap - 1) >> 1) & 1);
+  }
+  // The slot of every 16-key step of a segment's key tile: lanes 0..15 (-1:
+  // no such page; keys past the context need none).
+  __device__ __forceinline__ int slots_of(const Segment& g, int t) {
+    const int key = t * kKeys + lane * 16;
+    if (lane >= 16 || key >= g.r.ctx || t >= g.t1) return -1;
+    const int64_t page = __ldg(a.block_table + g.b * a.table_stride + (key >> a.page_shift));
+    if (page < 0 || page >= a.pages) {
+      report(a.err, TS_DEVERR_SLOT_RANGE);
+      return -1;
+    }
+    return static_cast<int>((page << a.page_shift) + (key & ((1 << a.page_shift) - 1)));
+  }
+  // This CTA's keys of a tile into L2, page by page: the stages read a row in
+  // nine or more pieces, one stage after another; from L2 they come sooner,
+  // and HBM sees whole pages.
+  __device__ __forceinline__ void prefetch(int slots, int row_bytes) {
+    if (slots >= 0 && lane >> 3 == int(rank) && (lane & (k_step - 1)) == 0)
+      prefetch_l2(a.cache + int64_t(slots) * row_bytes, k_step * 16 * row_bytes);
+  }
+  // Q of a row tile that starts at output row `row0`: by TMA (rows past the
+  // tile's are other rows' values, or zeros past the last; their scores are
+  // never used) ...
+  __device__ __forceinline__ void q_by_tma(int row0, int rows, uint32_t bar) {
+    const bool any = int(rank) * kRowsCta < rows;
+    if (!el) return;
+    if (any) {
+      mbar_expect_tx_cluster(bar, kQBytes);
+      tma_load_3d_pair(q_tile, &maps.q, bar, 0, row0 + rank * kRowsCta, 0);
+    } else {
+      mbar_arrive_cluster(bar);
+    }
+  }
+  // ... or, tokens further apart, row by row by `warps` warps.
+  template <bool k8>
+  __device__ __forceinline__ void q_by_copy(int row0, int rows, int w, int warps) {
+    for (int i = w; i < kRowsCta; i += warps) {
+      const int rr = rank * kRowsCta + i;
+      const bool valid = rr < rows;
+      const int row = row0 + (valid ? rr : 0);
+      const uint8_t* src =
+          a.q + int64_t(row / a.H) * a.q_stride + int64_t(row % a.H) * DSA_ROW_BYTES;
+      for (int c = lane; c < DSA_ROW_CHUNKS; c += 32) {
+        uint8_t* dst = q_tile + (c >> 3) * kQBlock + i * 128 + (((c & 7) ^ (i & 7)) << 4);
+        if (k8 && c < 64) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (valid) x = __ldg(reinterpret_cast<const uint4*>(src) + c);
+          *reinterpret_cast<uint4*>(dst) = code_order(x);
+        } else {
+          cp_async16_zfill(dst, src + c * 16, valid);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  // K stage: this CTA's 128 keys of a tile, 64 dims of block kb.
+  __device__ __forceinline__ void k_by_tma(int slots, int kb, uint8_t* dst, uint32_t bar) {
+    const uint32_t boxes = __popc(__ballot_sync(
+        0xffffffffu, slots >= 0 && lane >> 3 == int(rank) && (lane & (k_step - 1)) == 0));
+    if (el) mbar_expect_tx_cluster(bar, boxes * k_step * 2048);
+    for (int i = 0; i < 8; i += k_step) {
+      const int slot = __shfl_sync(0xffffffffu, slots, rank * 8 + i);
+      if (slot >= 0 && el) tma_load_3d_pair(dst + i * 2048, &maps.k, bar, 0, slot, kb);
+    }
+  }
+  // V stage: 64 keys from key0 on (group g of the tile), dims of blocks kb, kb + 1.
+  __device__ __forceinline__ void v_by_tma(int slots, int key0, int ctx, int g, int kb,
+                                           uint8_t* dst, uint32_t bar) {
+    const bool gaps = __any_sync(0xffffffffu, lane >> 2 == g && slots < 0);
+    if (key0 + 64 > ctx || gaps) {
+      // V rows that are not the request's must be zeros: their weights are,
+      // but the rows may hold anything, and 0 times NaN is NaN
+      for (int i = 0; i < 32; ++i) {
+        const int row = i * 2 + (lane >> 4), c = lane & 15;  // a row's 16 pieces
+        int slot = __shfl_sync(0xffffffffu, slots, g * 4 + (row >> 4));
+        const bool valid = key0 + row < ctx && slot >= 0;
+        slot = max(slot, 0) + (valid ? row & 15 : 0);
+        cp_async16_zfill(dst + (c >> 3) * kVBox + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                         a.cache + int64_t(slot) * DSA_ROW_BYTES + kb * 128 + c * 16, valid);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (el) mbar_arrive_cluster(bar);
+      return;
+    }
+    if (el) mbar_expect_tx_cluster(bar, kStageBytes);
+    for (int i = 0; i < 4; i += v_step) {
+      const int slot = __shfl_sync(0xffffffffu, slots, g * 4 + i);
+      if (el) {
+        tma_load_3d_pair(dst + i * 2048, &maps.v, bar, 0, slot, kb);
+        if (v_step < 4) tma_load_3d_pair(dst + kVBox + i * 2048, &maps.v, bar, 0, slot, kb + 1);
+      }
+    }
+  }
+};
+
+// The stages of a segment in the order the products take them: for each tile
+// t its nine K stages, then the V stages of tile t - 1 (64-key group v / 2,
+// dims half v % 2). Stages of phase t of a segment:
+__device__ __forceinline__ int stages_of(const Segment& g, int t) {
+  return (t < g.t1 ? kBlocks : 0) + (t > g.t0 ? 2 * groups(g.end, t - 1) : 0);
+}
+
+// bf16 rows: warp w of kTmaWarps.
+__device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
+  constexpr int kStages = Layout<DSA_CACHE_BF16>::kStages;
+  const Args& a = ld.a;
+  Segment sg;
+  static_assert(kTmaWarps <= 2 * kStages, "wait_free");
+  uint32_t s = 0, wrap = 0, qn = 0;
+  int turn = 0;  // whose stage is next
+  bool ok = true;
+  while (ok && walk.next(a, sg)) {
+    int here = -1, now = ld.slots_of(sg, sg.t0), next = ld.slots_of(sg, sg.t0 + 1);
+    if (w == 0) {
+      ld.prefetch(now, DSA_ROW_BYTES);
+      ld.prefetch(next, DSA_ROW_BYTES);
+    }
+    if (w == 0 || !a.q_dense) {
+      if (qn > 0) ok = ld.wait(&ld.bars->q_empty, (qn - 1) & 1);
+      if (!ok) break;
+      const int row0 = sg.r.q0 * a.H + sg.row0;
+      if (a.q_dense) {
+        ld.q_by_tma(row0, sg.rows, ld.q_full);
+      } else {
+        ld.q_by_copy<false>(row0, sg.rows, w, kTmaWarps);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ld.el) mbar_arrive_cluster(ld.q_full);
+      }
+    }
+    ++qn;
+    for (int t = sg.t0; t <= sg.t1 && ok; ++t) {
+      const bool scores = t < sg.t1;
+      const int ahead = ld.slots_of(sg, t + 2);
+      if (w == 0) {
+        ld.prefetch(ahead, DSA_ROW_BYTES);
+        if (t == sg.t1 - 1) {  // the next segment's first tile
+          Walk peek = walk;
+          Segment g;
+          if (peek.next(a, g)) ld.prefetch(ld.slots_of(g, g.t0), DSA_ROW_BYTES);
+        }
+      }
+      const int n = stages_of(sg, t);
+      for (int i = 0; i < n && ok; ++i) {
+        if (turn == w) {
+          ok = ld.wait_free(s, wrap);
+          if (ok) {
+            uint8_t* dst = ld.ring + s * kStageBytes;
+            const uint32_t bar = ld.full + s * 8;
+            if (scores && i < kBlocks) {
+              ld.k_by_tma(now, i, dst, bar);
+            } else {
+              const int v = scores ? i - kBlocks : i;
+              ld.v_by_tma(here, (t - 1) * kKeys + (v >> 1) * 64, sg.r.ctx, v >> 1,
+                          ld.rank * 4 + (v & 1) * 2, dst, bar);
+            }
+          }
+        }
+        if (++turn == kTmaWarps) turn = 0;
+        if (++s == kStages) s = 0, ++wrap;
+      }
+      here = now;
+      now = next;
+      next = ahead;
+    }
+  }
+}
+
+// 8-bit rows: Q, and the L2's prefetch, paced by the row tiles.
+__device__ __forceinline__ void load_q_8bit(Loader& ld, Walk walk) {
+  const Args& a = ld.a;
+  Segment sg;
+  uint32_t qn = 0;
+  bool ok = true;
+  while (ok && walk.next(a, sg)) {
+    if (a.q_dense) {
+      if (qn > 0) ok = ld.wait(&ld.bars->q_empty, (qn - 1) & 1);
+      if (!ok) break;
+      ld.q_by_tma(sg.r.q0 * a.H + sg.row0, sg.rows, dsmem_addr(&ld.bars->q_raw, ld.rank));
+    }
+    ++qn;
+  }
+}
+
+// 8-bit rows: warp w of kConvertWarps. A stage of codes is two halves of 64
+// keys x 64 dims; lane i takes row i / 4 of every eight, and 16 of the 64
+// codes. While a half is converted, the same half of the warp's next stage is
+// on its way into the space that it was read from.
+__device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
+  constexpr int kStages = Layout<DSA_CACHE_E4M3>::kStages;
+  const Args& a = ld.a;
+  Bars* bars = ld.bars;
+  const int r0 = ld.lane >> 2, c = ld.lane & 3;
+  uint8_t* raw = ld.raw + w * 2 * kRawHalf;
+  const uint8_t* read = raw + r0 * 64 + c * 16;
+  const uint32_t write0 = r0 * 128 + (((2 * c) ^ r0) << 4);
+  const uint32_t write1 = r0 * 128 + (((2 * c + 1) ^ r0) << 4);
+  // the stage in flight: its place in the ring, each half's keys (those of the
+  // context | valid 16-key steps << 8) and scales, and, if it is its segment's
+  // first of this warp, the row tile whose Q comes before it
+  bool have = false, first = false, rope = false;
+  int held = -1;  // a rope stage's slots
+  uint32_t at = 0, at_wrap = 0, raw_phase = 0, qn = 0;
+  int row0 = 0, rows = 0;
+  uint32_t keys[2] = {0, 0};
+  float scale[2][8];
+  // the walk over the stages
+  Segment sg;
+  bool inside = false, fresh = false, ok = true;
+  int t = 0, i = 0, n = 0, here = -1, now = -1, next = -1, turn = 0;
+  uint32_t s = 0, wrap = 0;
+  for (;;) {
+    // this warp's next stage: half h from 16-key steps step[h].. of `slots`,
+    // left[h] keys of the context, block kb[h]
+    bool more = false, more_rope = false;
+    int slots = -1, step[2] = {0, 0}, left[2] = {0, 0}, kb[2] = {0, 0};
+    uint32_t more_at = 0, more_wrap = 0;
+    while (!more) {
+      if (!inside) {
+        if (!walk.next(a, sg)) break;
+        inside = fresh = true;
+        t = sg.t0;
+        i = 0;
+        n = stages_of(sg, t);
+        here = -1;
+        now = ld.slots_of(sg, t);
+        next = ld.slots_of(sg, t + 1);
+        if (w == 0) {
+          ld.prefetch(now, kE4m3RowBytes);
+          ld.prefetch(next, kE4m3RowBytes);
+        }
+      }
+      for (; i < n && !more; ++i) {
+        if (turn == w) {
+          more = true;
+          more_at = s;
+          more_wrap = wrap;
+          if (t < sg.t1 && i < kBlocks) {
+            slots = now;
+            more_rope = i == kBlocks - 1;
+            step[0] = ld.rank * 8;
+            step[1] = step[0] + 4;
+            left[0] = sg.r.ctx - t * kKeys - int(ld.rank) * 128;
+            left[1] = left[0] - 64;
+            kb[0] = kb[1] = i;
+          } else {
+            const int v = t < sg.t1 ? i - kBlocks : i, g = v >> 1;
+            slots = here;
+            step[0] = step[1] = g * 4;
+            left[0] = left[1] = sg.r.ctx - (t - 1) * kKeys - g * 64;
+            kb[0] = ld.rank * 4 + (v & 1) * 2;
+            kb[1] = kb[0] + 1;
+          }
+        }
+        if (++turn == kConvertWarps) turn = 0;
+        if (++s == kStages) s = 0, ++wrap;
+      }
+      if (!more) {  // the phase is through
+        here = now;
+        now = next;
+        inside = ++t <= sg.t1;
+        if (inside) {
+          i = 0;
+          n = stages_of(sg, t);
+          next = ld.slots_of(sg, t + 1);
+          if (w == 0) ld.prefetch(next, kE4m3RowBytes);
+        }
+      }
+    }
+    if (!more && !have) break;
+    if (have && rope) {  // bf16 as it is, by TMA
+      ok = ld.wait_free(at, at_wrap);
+      if (ok) ld.k_by_tma(held, 0, ld.ring + at * kStageBytes, ld.full + at * 8);
+    }
+#pragma unroll
+    for (int h = 0; h < 2 && ok; ++h) {
+      uint4 code[8];
+      float f[8];
+      if (have && !rope) {
+        ok = ld.wait(&bars->raw[w][h], raw_phase);
+        if (!ok) break;
+        const bool whole = keys[h] == (64u | 0xf00u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          code[k] = *reinterpret_cast<const uint4*>(read + h * kRawHalf + k * 512);
+          if (!whole && !(r0 + 8 * k < int(keys[h] & 0xff) && (keys[h] >> (8 + (k >> 1)) & 1)))
+            code[k] = make_uint4(0, 0, 0, 0);
+          f[k] = scale[h][k];
+        }
+      }
+      __syncwarp();
+      if (more && !more_rope) {
+        uint32_t valid = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int slot = __shfl_sync(0xffffffffu, slots, step[h] + k);
+          valid |= (slot >= 0 ? 1u : 0u) << k;
+#pragma unroll
+          for (int j = 2 * k; j < 2 * k + 2; ++j) {
+            scale[h][j] = 1.f;
+            if (slot >= 0 && r0 + 8 * j < left[h])
+              scale[h][j] = __ldg(reinterpret_cast<const float*>(
+                                      a.cache + int64_t(slot + r0 + 8 * (j & 1)) * kE4m3RowBytes +
+                                      TS_D_LATENT) + (kb[h] >> 1));
+          }
+        }
+        keys[h] = static_cast<uint32_t>(min(max(left[h], 0), 64)) | valid << 8;
+        const uint32_t boxes = valid & (ld.v_step == 4 ? 1u : ld.v_step == 2 ? 5u : 15u);
+        if (ld.el) {
+          if (boxes) mbar_expect_tx(&bars->raw[w][h], __popc(boxes) * ld.v_step * 1024);
+          else mbar_arrive(&bars->raw[w][h]);
+        }
+        for (int k = 0; k < 4; k += ld.v_step) {
+          const int slot = __shfl_sync(0xffffffffu, slots, step[h] + k);
+          if (slot >= 0 && ld.el)
+            tma_load_3d(raw + h * kRawHalf + k * 1024, &ld.maps.code, &bars->raw[w][h], kb[h] * 64,
+                        slot, 0);
+        }
+      }
+      if (!have || rope) continue;
+      if (h == 0) {
+        if (first) {
+          if (a.q_dense) {
+            ok = ld.wait(&bars->q_raw, qn & 1);
+            for (int k = w * 32 + ld.lane; ok && k < kRowsCta * 64; k += kConvertWarps * 32) {
+              uint4* x = reinterpret_cast<uint4*>(ld.q_tile) + k;  // the eight latent blocks
+              *x = code_order(*x);
+            }
+          } else {
+            if (qn > 0) ok = ld.wait(&bars->q_empty, (qn - 1) & 1);
+            if (ok) ld.q_by_copy<true>(row0, rows, w, kConvertWarps);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (ok && ld.el) mbar_arrive_cluster(ld.q_full);
+          ++qn;
+        }
+        static_assert(kConvertWarps <= 2 * kStages, "wait_free");
+        ok = ok && ld.wait_free(at, at_wrap);
+        if (!ok) break;
+      }
+      uint8_t* dst = ld.ring + at * kStageBytes + h * kVBox;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        __nv_bfloat162 o[8];
+        widen_codes(code[k], o);
+        // 2^120 scale is past bf16's range for a scale above 2^7
+        const __nv_bfloat162 up =
+            __float2bfloat162_rn(f[k] > 128.f ? 0x1p120f : f[k] * 0x1p120f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = __hmul2(o[j], up);
+        if (__any_sync(0xffffffffu, f[k] > 128.f)) {
+          const __nv_bfloat162 rest = __float2bfloat162_rn(f[k] > 128.f ? f[k] : 1.f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = __hmul2(o[j], rest);
+        }
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(o);
+        *reinterpret_cast<uint4*>(dst + k * 1024 + write0) = make_uint4(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<uint4*>(dst + k * 1024 + write1) = make_uint4(u[4], u[5], u[6], u[7]);
+      }
+    }
+    if (!ok) break;
+    if (have && !rope) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (ld.el) mbar_arrive_cluster(ld.full + at * 8);
+      raw_phase ^= 1;
+    }
+    if (!more) break;
+    have = true;
+    at = more_at;
+    at_wrap = more_wrap;
+    rope = more_rope;
+    held = slots;
+    first = fresh;
+    if (fresh) {
+      row0 = sg.r.q0 * a.H + sg.row0;
+      rows = sg.rows;
+      fresh = false;
+    }
   }
 }
 
 template <int kFmt>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFmt), 1)
-    chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                 const Args a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThreads, 1)
+    chunk_kernel(const __grid_constant__ Maps maps, const Args a) {
+  using Lay = Layout<kFmt>;
+  constexpr int kStages = Lay::kStages, kMmaWarp = Lay::kMmaWarp;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Bars* bars = reinterpret_cast<Bars*>(smem_raw);
   uint8_t* q_tile = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + kBarBytes + 1023) & ~uintptr_t(1023));
   uint8_t* p_tile = q_tile + kQBytes;
   uint8_t* ring = p_tile + kPBytes;
-  constexpr int kLoaders = loader_warps(kFmt), kMmaWarp = kSoftmaxWarps + kLoaders;
-  constexpr int kRowBytes = cache_row_bytes(kFmt);
   volatile int* abort = &bars->abort;
   const int pair = blockIdx.x >> 1;
   const uint32_t rank = cluster_ctarank();
@@ -362,23 +795,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFmt), 1)
   const uint64_t wait_ns = a.wait_ns;
 
   launch_dependents();
-  if (blockIdx.x == 0) check_lengths(a);
-  plan(a, bars, pair);
-  if (bars->count == 0) {  // the same in both CTAs
-    if (rank == 0 && threadIdx.x < 2) a.meta[pair * 2 + threadIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
-  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->full[s], 2);
-      mbar_init(&bars->empty[s], 1);
+      mbar_init(&bars->empty[0][s], 1);
+      mbar_init(&bars->empty[1][s], 1);
     }
-    mbar_init(&bars->q_full, 2 * kLoaders);
+    mbar_init(&bars->q_full, Lay::k8 ? 2 * kConvertWarps : a.q_dense ? 2 : 2 * kTmaWarps);
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->s_full[0], 1);
     mbar_init(&bars->s_full[1], 1);
     mbar_init(&bars->p_full, 2 * kSoftmaxWarps);
     mbar_init(&bars->pv_done, 1);
+    for (int i = 0; i < 2 * kConvertWarps; ++i) mbar_init(&bars->raw[i >> 1][i & 1], 1);
+    mbar_init(&bars->q_raw, 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     mbar_fence_init();
@@ -387,8 +817,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFmt), 1)
     tmem_alloc_pair(&bars->tmem_slot, 512);
     tmem_relinquish_pair();
   }
+  if (blockIdx.x == 0) check_lengths(a);
+  plan(a, bars, pair);
   tc_fence_before();
-  __syncthreads();
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_slot;
@@ -399,7 +830,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFmt), 1)
     // ---------------- softmax and epilogue: two threads per TMEM lane ----------------
     // Lanes r and r + 64 hold row r: of S keys 0..127 and 128..255, of O dims
     // 0..255 and 256..511; of either, a lane's two threads take half the columns.
-    regs_inc<softmax_regs(kFmt)>();
+    regs_inc<Lay::kSoftmaxRegs>();
     const int L = (warp & 3) * 32 + lane, r = L & 63, half = L >> 6, part = warp >> 2;
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t p_full = dsmem_addr(&bars->p_full, 0);
@@ -558,223 +989,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFmt), 1)
     }
   } else if (warp < kMmaWarp) {
     // ---------------- loaders: Q, and the K and V stages in turn ----------------
-    regs_dec<other_regs(kFmt)>();
-    const int w = warp - kSoftmaxWarps;
-    const uint32_t q_full = dsmem_addr(&bars->q_full, 0);
-    const uint32_t full0 = dsmem_addr(&bars->full[0], 0);
-    uint32_t s = 0, phase = 1, qn = 0;  // a stage's first use waits for nothing
-    int turn = 0;                       // whose stage is next
-    bool ok = true;
-    const bool el = elect_one();
-    // 16-key steps that one TMA box of a K and of a V stage covers
-    const int k_step = min(8, (1 << a.page_shift) >> 4), v_step = min(4, k_step);
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_k);
-      if (kFmt == DSA_CACHE_BF16) tma_prefetch_desc(&tm_v);
-    }
-    // the slot of every 16-key step of a segment's key tile: lanes 0..15 (-1:
-    // no such page; keys past the context need none)
-    auto slots_of = [&](const Segment& g, int t) -> int {
-      const int key = t * kKeys + lane * 16;
-      if (lane >= 16 || key >= g.r.ctx || t >= g.t1) return -1;
-      const int64_t page = __ldg(a.block_table + g.b * a.table_stride + (key >> a.page_shift));
-      if (page < 0 || page >= a.pages) {
-        report(a.err, TS_DEVERR_SLOT_RANGE);
-        return -1;
-      }
-      return static_cast<int>((page << a.page_shift) + (key & ((1 << a.page_shift) - 1)));
-    };
-    // this CTA's keys of a tile into L2, page by page: the stages read a row
-    // in nine or more pieces, one stage after another; from L2 they come
-    // sooner, and HBM sees whole pages
-    auto prefetch = [&](int slots) {
-      if (w == 0 && slots >= 0 && lane >> 3 == int(rank) && (lane & (k_step - 1)) == 0)
-        prefetch_l2(a.cache + int64_t(slots) * kRowBytes, k_step * 16 * kRowBytes);
-    };
-    while (ok && walk.next(a, sg)) {
-      int here = -1, now = slots_of(sg, sg.t0), next = slots_of(sg, sg.t0 + 1);
-      prefetch(now);
-      prefetch(next);
-      // Q: rows past the tile's are zeros
-      if (qn > 0) ok = mbar_warp_wait<false>(&bars->q_empty, (qn - 1) & 1, abort, wait_ns);
-      if (!ok) break;
-      for (int i = w; i < kRowsCta; i += kLoaders) {
-        const int rr = rank * kRowsCta + i;
-        const bool valid = rr < sg.rows;
-        const int row = sg.row0 + (valid ? rr : 0);
-        const uint8_t* src = a.q + int64_t(sg.r.q0 + row / a.H) * a.q_stride +
-                             int64_t(row % a.H) * DSA_ROW_BYTES;
-#pragma unroll
-        for (int c0 = 0; c0 < DSA_ROW_CHUNKS; c0 += 32) {
-          const int c = c0 + lane;
-          uint8_t* dst = q_tile + (c >> 3) * kQBlock + i * 128 + (((c & 7) ^ (i & 7)) << 4);
-          if (kFmt == DSA_CACHE_E4M3 && c < 64) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (valid) x = __ldg(reinterpret_cast<const uint4*>(src) + c);
-            *reinterpret_cast<uint4*>(dst) =
-                make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632),
-                           __byte_perm(x.z, x.w, 0x5410), __byte_perm(x.z, x.w, 0x7632));
-          } else if (c < DSA_ROW_CHUNKS) {
-            cp_async16_zfill(dst, src + c * 16, valid);
-          }
-        }
-      }
-      bool q_pending = true;
-      auto q_landed = [&]() {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (el) mbar_arrive_cluster(q_full);
-        q_pending = false;
-      };
-      ++qn;
-
-      // K stage: this CTA's 128 keys of a tile, 64 dims of block kb
-      auto load_k = [&](int kb, uint32_t bytes, uint8_t* dst, uint32_t full) {
-        if (el) mbar_expect_tx_cluster(full, bytes);
-        for (int i = 0; i < 8; i += k_step) {
-          const int slot = __shfl_sync(0xffffffffu, now, rank * 8 + i);
-          if (slot >= 0 && el) tma_load_3d_pair(dst + i * 2048, &tm_k, full, 0, slot, kb);
-        }
-      };
-      // V stage: 64 keys of group g of tile t, dims of blocks kb and kb + 1
-      auto load_v = [&](int t, int g, int kb, uint8_t* dst, uint32_t full) {
-        const int key0 = t * kKeys + g * 64;
-        const bool gaps = __any_sync(0xffffffffu, lane >> 2 == g && here < 0);
-        if (key0 + 64 > sg.r.ctx || gaps) {
-          // V rows that are not the request's must be zeros: their weights
-          // are, but the rows may hold anything, and 0 times NaN is NaN
-          for (int i = 0; i < 32; ++i) {
-            const int row = i * 2 + (lane >> 4), c = lane & 15;  // a row's 16 pieces
-            int slot = __shfl_sync(0xffffffffu, here, g * 4 + (row >> 4));
-            const bool valid = key0 + row < sg.r.ctx && slot >= 0;
-            slot = max(slot, 0) + (valid ? row & 15 : 0);
-            cp_async16_zfill(dst + (c >> 3) * kVBox + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                             a.cache + int64_t(slot) * DSA_ROW_BYTES + kb * 128 + c * 16, valid);
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (el) mbar_arrive_cluster(full);
-          return;
-        }
-        if (el) mbar_expect_tx_cluster(full, kStageBytes);
-        for (int i = 0; i < 4; i += v_step) {
-          const int slot = __shfl_sync(0xffffffffu, here, g * 4 + i);
-          if (el) {
-            tma_load_3d_pair(dst + i * 2048, &tm_v, full, 0, slot, kb);
-            if (v_step < 4) tma_load_3d_pair(dst + kVBox + i * 2048, &tm_v, full, 0, slot, kb + 1);
-          }
-        }
-      };
-      // An 8-bit stage: two halves of 64 keys x 64 dims, half h from the four
-      // 16-key steps of `slots` from step on; keys from `count` on (and those
-      // of bad pages) are zeros. Lane i takes row i / 4 of every eight, and 16
-      // of the 64 codes. The codes are on their way before the stage is free.
-      auto load_codes = [&](int slots, int step0, int step1, int count0, int count1, int kb0,
-                            int kb1, uint8_t* dst, uint32_t full, uint64_t* empty) {
-        const int r0 = lane >> 2, c = lane & 3;
-        uint4 code[2][8];
-        float scale[2][8];
-        auto fetch = [&](const int h) {
-          const int step = h ? step1 : step0, count = h ? count1 : count0, kb = h ? kb1 : kb0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int slot = __shfl_sync(0xffffffffu, slots, step + (i >> 1));
-            code[h][i] = make_uint4(0, 0, 0, 0);
-            scale[h][i] = 1.f;
-            if (slot >= 0 && r0 + 8 * i < count) {
-              const uint8_t* src = a.cache + int64_t(slot + r0 + 8 * (i & 1)) * kE4m3RowBytes;
-              code[h][i] = __ldg(reinterpret_cast<const uint4*>(src + kb * 64) + c);
-              scale[h][i] = __ldg(reinterpret_cast<const float*>(src + TS_D_LATENT) + (kb >> 1));
-            }
-          }
-        };
-        auto store = [&](const int h) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            __nv_bfloat162 o[8];
-            widen_codes(code[h][i], o);
-            // 2^120 scale is past bf16's range for a scale above 2^7
-            const float up = scale[h][i] <= 128.f ? scale[h][i] * 0x1p120f : 0x1p120f;
-            const __nv_bfloat162 f = __float2bfloat162_rn(up);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = __hmul2(o[k], f);
-            if (__any_sync(0xffffffffu, scale[h][i] > 128.f)) {
-              const __nv_bfloat162 f2 =
-                  __float2bfloat162_rn(scale[h][i] <= 128.f ? 1.f : scale[h][i]);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = __hmul2(o[k], f2);
-            }
-            const uint32_t* u = reinterpret_cast<const uint32_t*>(o);
-            uint8_t* row = dst + h * kVBox + (r0 + 8 * i) * 128;
-            *reinterpret_cast<uint4*>(row + (((2 * c) ^ r0) << 4)) =
-                make_uint4(u[0], u[1], u[2], u[3]);
-            *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ r0) << 4)) =
-                make_uint4(u[4], u[5], u[6], u[7]);
-          }
-        };
-        fetch(0);
-        ok = mbar_warp_wait<false>(empty, phase, abort, wait_ns);
-        if (!ok) return;
-        fetch(1);
-        store(0);
-        store(1);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (el) mbar_arrive_cluster(full);
-      };
-      // the stages in the order the products take them, dealt to the warps in turn
-      for (int t = sg.t0; t <= sg.t1 && ok; ++t) {
-        const bool scores = t < sg.t1;
-        const int ahead = slots_of(sg, t + 2);
-        prefetch(ahead);
-        if (t == sg.t1 - 1 && w == 0) {  // the next segment's first tile
-          Walk peek = walk;
-          Segment g;
-          if (peek.next(a, g)) prefetch(slots_of(g, g.t0));
-        }
-        const uint32_t boxes = __popc(__ballot_sync(
-            0xffffffffu, now >= 0 && lane >> 3 == int(rank) && (lane & (k_step - 1)) == 0));
-        const int n = (scores ? kBlocks : 0) + (t > sg.t0 ? 2 * groups(sg.end, t - 1) : 0);
-        for (int i = 0; i < n && ok; ++i) {
-          if (turn == w) {
-            uint8_t* dst = ring + s * kStageBytes;
-            const uint32_t full = full0 + s * 8;
-            const bool is_k = scores && i < kBlocks;
-            const int v = scores ? i - kBlocks : i;  // V: group v / 2, dims half v % 2
-            const int vb = rank * 4 + (v & 1) * 2;
-            if (kFmt == DSA_CACHE_E4M3 && !(is_k && i == kBlocks - 1)) {
-              if (is_k) {
-                const int left = sg.r.ctx - t * kKeys - int(rank) * 128;
-                load_codes(now, rank * 8, rank * 8 + 4, left, left - 64, i, i, dst, full,
-                           &bars->empty[s]);
-              } else {
-                const int g = v >> 1, left = sg.r.ctx - (t - 1) * kKeys - g * 64;
-                load_codes(here, g * 4, g * 4, left, left, vb, vb + 1, dst, full, &bars->empty[s]);
-              }
-            } else {
-              ok = mbar_warp_wait<false>(&bars->empty[s], phase, abort, wait_ns);
-              if (ok) {
-                // (the 8-bit format's rope part is bf16: its map has one block)
-                if (is_k) load_k(kFmt == DSA_CACHE_E4M3 ? 0 : i, boxes * k_step * 2048, dst, full);
-                else load_v(t - 1, v >> 1, vb, dst, full);
-              }
-            }
-            // Q's copies landed beside this warp's first stage (its second may
-            // wait for products, and they for Q)
-            if (q_pending) q_landed();
-          }
-          if (++turn == kLoaders) turn = 0;
-          if (++s == kStages) s = 0, phase ^= 1;
-        }
-        here = now;
-        now = next;
-        next = ahead;
-      }
-    }
+    regs_dec<Lay::kOtherRegs>();
+    const int w = warp - kSoftmaxWarps, k_step = min(8, (1 << a.page_shift) >> 4);
+    Loader ld{a, maps, bars, q_tile, ring, ring + kStages * kStageBytes, rank,
+              dsmem_addr(&bars->q_full, 0), dsmem_addr(&bars->full[0], 0), lane, elect_one(),
+              abort, k_step, min(4, k_step)};
+    if (!Lay::k8) load_bf16(ld, walk, w);
+    else if (w == kConvertWarps) load_q_8bit(ld, walk);
+    else load_codes(ld, walk, w);
   } else {
-    regs_dec<other_regs(kFmt)>();
+    regs_dec<Lay::kOtherRegs>();
     if (rank == 0) {
       // ---------------- MMA issuer (the even CTA's, for both) ----------------
       // a negative scale negates Q (its bit of the instruction descriptor)
@@ -831,7 +1055,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFmt), 1)
 #pragma unroll
                   for (int kk = 0; kk < 4; ++kk)
                     tc_mma_bf16_pair(d, qd + kk * 2, kd + kk * 2, id_s, (kb | i | kk) != 0);
-                  tc_commit_pair(&bars->empty[s]);
+                  tc_commit_pair(&bars->empty[phase][s]);
                 }
                 advance();
               }
@@ -861,7 +1085,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFmt), 1)
                   for (int kk = 0; kk < 4; ++kk)
                     tc_mma_bf16_pair(tmem + kOCol + j * 128, pd + kk * 2, vd + kk * (2048 >> 4),
                                      id_pv, !first || (g | kk) != 0);
-                  tc_commit_pair(&bars->empty[s]);
+                  tc_commit_pair(&bars->empty[phase][s]);
                 }
                 advance();
               }
@@ -977,18 +1201,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Arg
 
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// 3-D map over cache rows of blocks of 64 bf16: dims {64, rows, blocks}; box
-// {64, box_rows, box_blocks}.
+// 3-D map over rows of `blocks` blocks of `inner` values: dims {inner, rows,
+// blocks}; box {64, box_rows, box_blocks}. bf16 values, swizzled by 128 bytes,
+// or (codes) plain bytes.
 bool make_map(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_bytes,
-              uint64_t blocks, uint32_t box_rows, uint32_t box_blocks) {
+              uint64_t inner, uint64_t blocks, uint32_t box_rows, uint32_t box_blocks,
+              bool codes = false) {
   EncodeTiled enc = tensor_map_encoder();
   if (!enc) return false;
-  const cuuint64_t dims[3] = {64, rows, blocks};
+  const cuuint64_t dims[3] = {inner, rows, blocks};
   const cuuint64_t strides[2] = {row_bytes, 128};
   const cuuint32_t box[3] = {64, box_rows, box_blocks};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return enc(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -996,12 +1223,12 @@ int part_rows(int T, int H) { return static_cast<int>(std::min(int64_t(T) * H, i
 
 // The attention's launch; the maps and the merge are the caller's.
 template <int kFmt>
-ts_status launch_chunk(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Args& a,
-                       cudaStream_t stream) {
+ts_status launch_chunk(const Maps& maps, const Args& a, cudaStream_t stream) {
+  using Lay = Layout<kFmt>;
   static std::atomic<uint64_t> smem_set{0};
-  if (!raise_smem_limit(reinterpret_cast<const void*>(chunk_kernel<kFmt>), kSmemBytes, smem_set))
+  if (!raise_smem_limit(reinterpret_cast<const void*>(chunk_kernel<kFmt>), Lay::kSmem, smem_set))
     return TS_ERR_CUDA;
-  chunk_kernel<kFmt><<<2 * a.pairs, threads_of(kFmt), kSmemBytes, stream>>>(tm_k, tm_v, a);
+  chunk_kernel<kFmt><<<2 * a.pairs, Lay::kThreads, Lay::kSmem, stream>>>(maps, a);
   return launch_status();
 }
 
@@ -1038,6 +1265,7 @@ extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_
   Args a = {};
   a.q = static_cast<const uint8_t*>(q);
   a.q_stride = q_stride * 2;
+  a.q_dense = q_stride == int64_t(H) * DSA_D || T == 1;
   a.cu_q = cu_q;
   a.T = T;
   a.B = B;
@@ -1064,18 +1292,23 @@ extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_
   a.opart = reinterpret_cast<float*>(w);
   a.wait_ns = wait_limit_ns(kWaitLimit);
   a.err = err;
-  CUtensorMap tm_k, tm_v;
+  Maps maps = {};
+  bool made = !a.q_dense || make_map(&maps.q, q, int64_t(T) * H, DSA_ROW_BYTES, 64, kBlocks,
+                                     kRowsCta, kBlocks);
   if (fmt == DSA_CACHE_BF16) {
-    if (!make_map(&tm_k, cache, num_slots, DSA_ROW_BYTES, kBlocks, std::min(page_size, 128), 1) ||
-        !make_map(&tm_v, cache, num_slots, DSA_ROW_BYTES, kBlocks, std::min(page_size, 64),
-                  page_size >= 64 ? 2 : 1))
-      return TS_ERR_CUDA;
-    st = launch_chunk<DSA_CACHE_BF16>(tm_k, tm_v, a, stream);
+    made = made &&
+           make_map(&maps.k, cache, num_slots, DSA_ROW_BYTES, 64, kBlocks, std::min(page_size, 128),
+                    1) &&
+           make_map(&maps.v, cache, num_slots, DSA_ROW_BYTES, 64, kBlocks, std::min(page_size, 64),
+                    page_size >= 64 ? 2 : 1);
+    st = made ? launch_chunk<DSA_CACHE_BF16>(maps, a, stream) : TS_ERR_CUDA;
   } else {
-    if (!make_map(&tm_k, a.cache + kE4m3Rope, num_slots, kE4m3RowBytes, 1,
-                  std::min(page_size, 128), 1))
-      return TS_ERR_CUDA;
-    st = launch_chunk<DSA_CACHE_E4M3>(tm_k, tm_k, a, stream);
+    made = made &&
+           make_map(&maps.k, a.cache + kE4m3Rope, num_slots, kE4m3RowBytes, 64, 1,
+                    std::min(page_size, 128), 1) &&
+           make_map(&maps.code, cache, num_slots, kE4m3RowBytes, TS_D_LATENT, 1,
+                    std::min(page_size, 64), 1, true);
+    st = made ? launch_chunk<DSA_CACHE_E4M3>(maps, a, stream) : TS_ERR_CUDA;
   }
   if (st != TS_OK) return st;
   cudaLaunchConfig_t cfg = {};
