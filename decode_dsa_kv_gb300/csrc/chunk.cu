@@ -42,9 +42,8 @@ constexpr uint32_t kVBox = 64 * 128;     // V: 64 keys x 64 dims
 constexpr uint32_t kBarBytes = 3072;
 constexpr int kSoftmaxWarps = 8;  // warps 0..7: two threads per TMEM lane
 // bf16 rows: warps 8..10 load by TMA (every third stage each), warp 11 issues
-// the products. 8-bit rows: warps 8..13 convert (every sixth stage each, from
-// two halves of a stage's codes that each warp keeps in flight), warp 14 loads
-// Q, warp 15 issues the products.
+// the products. 8-bit rows: warps 8..13 convert (every sixth half of a stage
+// each, two of them in flight), warp 14 loads Q, warp 15 issues the products.
 constexpr int kTmaWarps = 3, kConvertWarps = 6;
 constexpr uint32_t kRawHalf = 4096;  // 64 keys x 64 codes
 template <int kFmt>
@@ -60,7 +59,7 @@ struct Layout {
   static_assert(kSmem <= 227 * 1024, "dynamic shared memory of one CTA");
   // Registers a thread after the split: the softmax's two warpgroups take what
   // the others give back (of 384 x 168, or 512 x 128, at launch).
-  static constexpr int kSoftmaxRegs = k8 ? 152 : 208, kOtherRegs = k8 ? 104 : 88;
+  static constexpr int kSoftmaxRegs = k8 ? 136 : 200, kOtherRegs = k8 ? 120 : 104;
   static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <=
                     kThreads * (k8 ? 128 : 168), "register split");
 };
@@ -86,7 +85,7 @@ struct Bars {
   uint64_t s_full[2];       // both: a tile's scores are complete
   uint64_t p_full;          // even CTA: P written and S read in both CTAs
   uint64_t pv_done;         // both: a tile's value products are complete
-  uint64_t raw[kConvertWarps][2];  // a converting warp's half-stages of codes
+  uint64_t raw[kConvertWarps][2];  // a converting warp's units of codes
   uint64_t q_raw;                  // Q as loaded (8-bit rows: reordered before use)
   uint64_t drain;
   uint64_t sum[16];
@@ -327,21 +326,28 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
-// 16 e4m3 codes as bf16 values times 2^-120, each four in the order 0, 2, 1, 3
-// (the scale's product brings the 2^120 back). A code's sign, exponent and
-// mantissa bits are moved into a bf16's places; a subnormal code becomes a
-// bf16 subnormal of the same value, so no code is special but NaN (which the
-// cache may not hold below ctx_len). The order costs nothing: Q's latent part
-// is laid out alike, and the epilogue names the output's registers alike.
-__device__ __forceinline__ void widen_codes(const uint4& c, __nv_bfloat162 (&o)[8]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t even = ((w[i] << 8) & 0x80008000u) | ((w[i] << 4) & 0x07f007f0u);
-    const uint32_t odd = (w[i] & 0x80008000u) | ((w[i] >> 4) & 0x07f007f0u);
-    o[2 * i] = *reinterpret_cast<const __nv_bfloat162*>(&even);
-    o[2 * i + 1] = *reinterpret_cast<const __nv_bfloat162*>(&odd);
-  }
+// 8 bf16 values times a power of two.
+__device__ __forceinline__ uint4 scaled(const uint4& x, float f) {
+  const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
+  auto mul = [&](uint32_t v) {
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), f2);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  };
+  return make_uint4(mul(x.x), mul(x.y), mul(x.z), mul(x.w));
+}
+
+// 16 e4m3 codes times 2^-120 f as bf16 values, each four in the order 0, 2, 1,
+// 3 (f is 2^120 times the codes' scale). A code's sign, exponent and mantissa
+// bits are moved into a bf16's places; a subnormal code becomes a bf16
+// subnormal of the same value, so no code is special but NaN (which the cache
+// may not hold below ctx_len). 9 instructions for four codes; through the
+// conversions to half and float it is 12. The order costs nothing: Q's latent
+// part is laid out alike, and the epilogue names the output's registers alike.
+__device__ __forceinline__ void widen_codes(const uint4& c, float f, uint4 (&o)[2]) {
+  auto even = [](uint32_t w) { return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u); };
+  auto odd = [](uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u); };
+  o[0] = scaled(make_uint4(even(c.x), odd(c.x), even(c.y), odd(c.y)), f);
+  o[1] = scaled(make_uint4(even(c.z), odd(c.z), even(c.w), odd(c.w)), f);
 }
 
 // 8 bf16 values, each four in the order of widen_codes.
@@ -365,7 +371,8 @@ __device__ __forceinline__ void natural_order(uint32_t (&v)[32]) {
 
 struct Maps {
   CUtensorMap q;     // [T H rows][9 blocks of 64], box 64 rows x 9 blocks
-  CUtensorMap k;     // cache rows, box min(page, 128) rows x 1 block (8-bit rows: the rope part)
+  CUtensorMap k;     // cache rows, box min(page, 128) rows x 1 block; 8-bit rows: their rope
+                     // part, box min(page, 64) rows
   CUtensorMap v;     // cache rows, box min(page, 64) rows x 2 blocks (1 below 64)
   CUtensorMap code;  // 8-bit rows: the codes, box min(page, 64) rows x 64
 };
@@ -426,7 +433,6 @@ struct Loader {
     }
   }
   // ... or, tokens further apart, row by row by `warps` warps.
-  template <bool k8>
   __device__ __forceinline__ void q_by_copy(int row0, int rows, int w, int warps) {
     for (int i = w; i < kRowsCta; i += warps) {
       const int rr = rank * kRowsCta + i;
@@ -434,16 +440,9 @@ struct Loader {
       const int row = row0 + (valid ? rr : 0);
       const uint8_t* src =
           a.q + int64_t(row / a.H) * a.q_stride + int64_t(row % a.H) * DSA_ROW_BYTES;
-      for (int c = lane; c < DSA_ROW_CHUNKS; c += 32) {
-        uint8_t* dst = q_tile + (c >> 3) * kQBlock + i * 128 + (((c & 7) ^ (i & 7)) << 4);
-        if (k8 && c < 64) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (valid) x = __ldg(reinterpret_cast<const uint4*>(src) + c);
-          *reinterpret_cast<uint4*>(dst) = code_order(x);
-        } else {
-          cp_async16_zfill(dst, src + c * 16, valid);
-        }
-      }
+      for (int c = lane; c < DSA_ROW_CHUNKS; c += 32)
+        cp_async16_zfill(q_tile + (c >> 3) * kQBlock + i * 128 + (((c & 7) ^ (i & 7)) << 4),
+                         src + c * 16, valid);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
@@ -518,7 +517,7 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
       if (a.q_dense) {
         ld.q_by_tma(row0, sg.rows, ld.q_full);
       } else {
-        ld.q_by_copy<false>(row0, sg.rows, w, kTmaWarps);
+        ld.q_by_copy(row0, sg.rows, w, kTmaWarps);
         fence_proxy_async_smem();
         __syncwarp();
         if (ld.el) mbar_arrive_cluster(ld.q_full);
@@ -562,62 +561,69 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
   }
 }
 
-// 8-bit rows: Q, and the L2's prefetch, paced by the row tiles.
+// 8-bit rows: Q of every row tile.
 __device__ __forceinline__ void load_q_8bit(Loader& ld, Walk walk) {
   const Args& a = ld.a;
   Segment sg;
   uint32_t qn = 0;
-  bool ok = true;
-  while (ok && walk.next(a, sg)) {
+  while (walk.next(a, sg)) {
+    if (qn > 0 && !ld.wait(&ld.bars->q_empty, (qn - 1) & 1)) break;
+    const int row0 = sg.r.q0 * a.H + sg.row0;
     if (a.q_dense) {
-      if (qn > 0) ok = ld.wait(&ld.bars->q_empty, (qn - 1) & 1);
-      if (!ok) break;
-      ld.q_by_tma(sg.r.q0 * a.H + sg.row0, sg.rows, dsmem_addr(&ld.bars->q_raw, ld.rank));
+      ld.q_by_tma(row0, sg.rows, dsmem_addr(&ld.bars->q_raw, ld.rank));
+    } else {
+      ld.q_by_copy(row0, sg.rows, 0, 1);
+      __syncwarp();
+      if (ld.el) mbar_arrive(&ld.bars->q_raw);
     }
     ++qn;
   }
 }
 
-// 8-bit rows: warp w of kConvertWarps. A stage of codes is two halves of 64
-// keys x 64 dims; lane i takes row i / 4 of every eight, and 16 of the 64
-// codes. While a half is converted, the same half of the warp's next stage is
-// on its way into the space that it was read from.
+// 8-bit rows: warp w of kConvertWarps. A stage is two units, its halves of 64
+// keys x 64 dims, dealt to the warps in turn; lane i takes row i / 4 of every
+// eight, and 16 of the 64 codes. Two units of a warp are in flight: their
+// codes (by TMA, into the warp's two raw spaces) and scales; a unit's space is
+// sent for again as soon as its codes are converted. A stage takes a warp some
+// 1500 clocks, so it is the units, not the stages, that are dealt: a place of
+// the ring is held that much shorter.
 __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
   constexpr int kStages = Layout<DSA_CACHE_E4M3>::kStages;
+  static_assert((kConvertWarps + 1) / 2 <= 2 * kStages, "wait_free");
   const Args& a = ld.a;
   Bars* bars = ld.bars;
   const int r0 = ld.lane >> 2, c = ld.lane & 3;
-  uint8_t* raw = ld.raw + w * 2 * kRawHalf;
-  const uint8_t* read = raw + r0 * 64 + c * 16;
+  const uint32_t read = w * 2 * kRawHalf + r0 * 64 + c * 16;
   const uint32_t write0 = r0 * 128 + (((2 * c) ^ r0) << 4);
   const uint32_t write1 = r0 * 128 + (((2 * c + 1) ^ r0) << 4);
-  // the stage in flight: its place in the ring, each half's keys (those of the
-  // context | valid 16-key steps << 8) and scales, and, if it is its segment's
-  // first of this warp, the row tile whose Q comes before it
-  bool have = false, first = false, rope = false;
-  int held = -1;  // a rope stage's slots
-  uint32_t at = 0, at_wrap = 0, raw_phase = 0, qn = 0;
-  int row0 = 0, rows = 0;
-  uint32_t keys[2] = {0, 0};
+  // a unit in flight: its keys of the context (bits 0..6), its valid 16-key
+  // steps (8..11), half (12), place (13..15), whether it is rope (16), whether
+  // Q comes before it (17), the place's use (18..); its slots; its scales
+  constexpr uint32_t kRope = 1u << 16, kFirst = 1u << 17;
+  uint32_t info[2];
+  int unit_slots[2];
   float scale[2][8];
+  int flying = 0;       // units in flight: the older one is number 0
+  uint32_t units = 0, sent = 0, qn = 0;
   // the walk over the stages
   Segment sg;
-  bool inside = false, fresh = false, ok = true;
+  bool inside = false, fresh = false, more_to_come = true;
   int t = 0, i = 0, n = 0, here = -1, now = -1, next = -1, turn = 0;
   uint32_t s = 0, wrap = 0;
   for (;;) {
-    // this warp's next stage: half h from 16-key steps step[h].. of `slots`,
-    // left[h] keys of the context, block kb[h]
-    bool more = false, more_rope = false;
-    int slots = -1, step[2] = {0, 0}, left[2] = {0, 0}, kb[2] = {0, 0};
-    uint32_t more_at = 0, more_wrap = 0;
-    while (!more) {
+    // this warp's next unit: 16-key steps step .. of `slots`, `left` keys of
+    // the context, block kb
+    bool more = false;
+    int slots = -1, step = 0, left = 0, kb = 0;
+    uint32_t word = 0;
+    while (!more && more_to_come) {
       if (!inside) {
-        if (!walk.next(a, sg)) break;
+        more_to_come = walk.next(a, sg);
+        if (!more_to_come) break;
         inside = fresh = true;
         t = sg.t0;
         i = 0;
-        n = stages_of(sg, t);
+        n = 2 * stages_of(sg, t);
         here = -1;
         now = ld.slots_of(sg, t);
         next = ld.slots_of(sg, t + 1);
@@ -627,29 +633,28 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
         }
       }
       for (; i < n && !more; ++i) {
+        const int h = i & 1;
         if (turn == w) {
           more = true;
-          more_at = s;
-          more_wrap = wrap;
-          if (t < sg.t1 && i < kBlocks) {
+          int v = i >> 1;
+          word = h << 12 | s << 13 | wrap << 18 | (fresh ? kFirst : 0u);
+          if (t < sg.t1 && v < kBlocks) {
             slots = now;
-            more_rope = i == kBlocks - 1;
-            step[0] = ld.rank * 8;
-            step[1] = step[0] + 4;
-            left[0] = sg.r.ctx - t * kKeys - int(ld.rank) * 128;
-            left[1] = left[0] - 64;
-            kb[0] = kb[1] = i;
+            step = ld.rank * 8 + h * 4;
+            left = sg.r.ctx - t * kKeys - int(ld.rank) * 128 - h * 64;
+            kb = v;
+            if (v == kBlocks - 1) word |= kRope;
           } else {
-            const int v = t < sg.t1 ? i - kBlocks : i, g = v >> 1;
+            v -= t < sg.t1 ? kBlocks : 0;  // 64-key group v / 2, dims half v % 2
             slots = here;
-            step[0] = step[1] = g * 4;
-            left[0] = left[1] = sg.r.ctx - (t - 1) * kKeys - g * 64;
-            kb[0] = ld.rank * 4 + (v & 1) * 2;
-            kb[1] = kb[0] + 1;
+            step = (v >> 1) * 4;
+            left = sg.r.ctx - (t - 1) * kKeys - (v >> 1) * 64;
+            kb = ld.rank * 4 + (v & 1) * 2 + h;
           }
+          fresh = false;
         }
         if (++turn == kConvertWarps) turn = 0;
-        if (++s == kStages) s = 0, ++wrap;
+        if (h && ++s == kStages) s = 0, ++wrap;
       }
       if (!more) {  // the phase is through
         here = now;
@@ -657,129 +662,128 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
         inside = ++t <= sg.t1;
         if (inside) {
           i = 0;
-          n = stages_of(sg, t);
+          n = 2 * stages_of(sg, t);
           next = ld.slots_of(sg, t + 1);
           if (w == 0) ld.prefetch(next, kE4m3RowBytes);
         }
       }
     }
-    if (!more && !have) break;
-    if (have && rope) {  // bf16 as it is, by TMA
-      ok = ld.wait_free(at, at_wrap);
-      if (ok) ld.k_by_tma(held, 0, ld.ring + at * kStageBytes, ld.full + at * 8);
-    }
-#pragma unroll
-    for (int h = 0; h < 2 && ok; ++h) {
-      uint4 code[8];
-      float f[8];
-      if (have && !rope) {
-        ok = ld.wait(&bars->raw[w][h], raw_phase);
-        if (!ok) break;
-        const bool whole = keys[h] == (64u | 0xf00u);
+    if (flying == 0 && !more) break;
+
+    // convert the older unit, once two are in flight or none follows
+    if (flying == 2 || !more) {
+      const uint32_t at = info[0] >> 13 & 7, half = info[0] >> 12 & 1;
+      if (info[0] & kFirst) {  // Q's latent part into the codes' order
+        if (!ld.wait(&bars->q_raw, qn & 1)) break;
+        ++qn;
+        for (int k = w * 32 + ld.lane; k < kRowsCta * 64; k += kConvertWarps * 32) {
+          uint4* x = reinterpret_cast<uint4*>(ld.q_tile) + k;
+          *x = code_order(*x);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ld.el) mbar_arrive_cluster(ld.q_full);
+      }
+      if (!ld.wait_free(at, info[0] >> 18)) break;
+      uint8_t* dst = ld.ring + at * kStageBytes + half * kVBox;
+      const uint32_t bar = ld.full + at * 8, valid = info[0] >> 8 & 15;
+      if (info[0] & kRope) {  // bf16 as it is, by TMA
+        const uint32_t boxes = valid & (ld.v_step == 4 ? 1u : ld.v_step == 2 ? 5u : 15u);
+        if (ld.el) mbar_expect_tx_cluster(bar, __popc(boxes) * ld.v_step * 2048);
+        for (int k = 0; k < 4; k += ld.v_step) {
+          const int slot = __shfl_sync(0xffffffffu, unit_slots[0], ld.rank * 8 + half * 4 + k);
+          if (slot >= 0 && ld.el) tma_load_3d_pair(dst + k * 2048, &ld.maps.k, bar, 0, slot, 0);
+        }
+      } else {
+        const uint32_t space = units & 1;
+        if (!ld.wait(&bars->raw[w][space], units >> 1 & 1)) break;
+        ++units;
+        const uint8_t* src = ld.raw + read + space * kRawHalf;
+        const int count = info[0] & 0x7f;
+        const bool whole = count == 64 && valid == 15;
+        float top = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          code[k] = *reinterpret_cast<const uint4*>(read + h * kRawHalf + k * 512);
-          if (!whole && !(r0 + 8 * k < int(keys[h] & 0xff) && (keys[h] >> (8 + (k >> 1)) & 1)))
-            code[k] = make_uint4(0, 0, 0, 0);
-          f[k] = scale[h][k];
+          // keys that are not the request's: codes of 0 and a scale that is no NaN
+          if (!whole && !(r0 + 8 * k < count && (valid >> (k >> 1) & 1))) scale[0][k] = 0.f;
+          top = fmaxf(top, scale[0][k]);
         }
-      }
-      __syncwarp();
-      if (more && !more_rope) {
-        uint32_t valid = 0;
+        // 2^120 scale is past bf16's range for a scale above 2^7
+        const bool big = __any_sync(0xffffffffu, top > 128.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int slot = __shfl_sync(0xffffffffu, slots, step[h] + k);
-          valid |= (slot >= 0 ? 1u : 0u) << k;
+        for (int k = 0; k < 8; ++k) {
+          uint4 code = *reinterpret_cast<const uint4*>(src + k * 512);
+          if (!whole && scale[0][k] == 0.f) code = make_uint4(0, 0, 0, 0);
+          uint4 o[2];
+          widen_codes(code, big ? 0x1p120f : scale[0][k] * 0x1p120f, o);
+          if (big) {
+            o[0] = scaled(o[0], scale[0][k]);
+            o[1] = scaled(o[1], scale[0][k]);
+          }
+          *reinterpret_cast<uint4*>(dst + k * 1024 + write0) = o[0];
+          *reinterpret_cast<uint4*>(dst + k * 1024 + write1) = o[1];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ld.el) mbar_arrive_cluster(bar);
+      }
+      --flying;
+      info[0] = info[1];
+      unit_slots[0] = unit_slots[1];
 #pragma unroll
-          for (int j = 2 * k; j < 2 * k + 2; ++j) {
-            scale[h][j] = 1.f;
-            if (slot >= 0 && r0 + 8 * j < left[h])
-              scale[h][j] = __ldg(reinterpret_cast<const float*>(
-                                      a.cache + int64_t(slot + r0 + 8 * (j & 1)) * kE4m3RowBytes +
-                                      TS_D_LATENT) + (kb[h] >> 1));
-          }
-        }
-        keys[h] = static_cast<uint32_t>(min(max(left[h], 0), 64)) | valid << 8;
-        const uint32_t boxes = valid & (ld.v_step == 4 ? 1u : ld.v_step == 2 ? 5u : 15u);
-        if (ld.el) {
-          if (boxes) mbar_expect_tx(&bars->raw[w][h], __popc(boxes) * ld.v_step * 1024);
-          else mbar_arrive(&bars->raw[w][h]);
-        }
-        for (int k = 0; k < 4; k += ld.v_step) {
-          const int slot = __shfl_sync(0xffffffffu, slots, step[h] + k);
-          if (slot >= 0 && ld.el)
-            tma_load_3d(raw + h * kRawHalf + k * 1024, &ld.maps.code, &bars->raw[w][h], kb[h] * 64,
-                        slot, 0);
-        }
+      for (int k = 0; k < 8; ++k) scale[0][k] = scale[1][k];
+    }
+    if (!more) continue;
+
+    // send for the new one
+    uint32_t valid = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      valid |= (__shfl_sync(0xffffffffu, slots, step + k) >= 0 ? 1u : 0u) << k;
+    word |= static_cast<uint32_t>(min(max(left, 0), 64)) | valid << 8;
+    float fresh_scale[8];
+    if (!(word & kRope)) {
+      const uint32_t space = sent & 1;
+      ++sent;
+      uint64_t* bar = &bars->raw[w][space];
+      const uint32_t boxes = valid & (ld.v_step == 4 ? 1u : ld.v_step == 2 ? 5u : 15u);
+      if (ld.el) {
+        if (boxes) mbar_expect_tx(bar, __popc(boxes) * ld.v_step * 1024);
+        else mbar_arrive(bar);
       }
-      if (!have || rope) continue;
-      if (h == 0) {
-        if (first) {
-          if (a.q_dense) {
-            ok = ld.wait(&bars->q_raw, qn & 1);
-            for (int k = w * 32 + ld.lane; ok && k < kRowsCta * 64; k += kConvertWarps * 32) {
-              uint4* x = reinterpret_cast<uint4*>(ld.q_tile) + k;  // the eight latent blocks
-              *x = code_order(*x);
-            }
-          } else {
-            if (qn > 0) ok = ld.wait(&bars->q_empty, (qn - 1) & 1);
-            if (ok) ld.q_by_copy<true>(row0, rows, w, kConvertWarps);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (ok && ld.el) mbar_arrive_cluster(ld.q_full);
-          ++qn;
-        }
-        static_assert(kConvertWarps <= 2 * kStages, "wait_free");
-        ok = ok && ld.wait_free(at, at_wrap);
-        if (!ok) break;
+      for (int k = 0; k < 4; k += ld.v_step) {
+        const int slot = __shfl_sync(0xffffffffu, slots, step + k);
+        if (slot >= 0 && ld.el)
+          tma_load_3d(ld.raw + (w * 2 + space) * kRawHalf + k * 1024, &ld.maps.code, bar, kb * 64,
+                      slot, 0);
       }
-      uint8_t* dst = ld.ring + at * kStageBytes + h * kVBox;
+      const uint8_t* scales = a.cache + TS_D_LATENT + (kb >> 1) * 4;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        __nv_bfloat162 o[8];
-        widen_codes(code[k], o);
-        // 2^120 scale is past bf16's range for a scale above 2^7
-        const __nv_bfloat162 up =
-            __float2bfloat162_rn(f[k] > 128.f ? 0x1p120f : f[k] * 0x1p120f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = __hmul2(o[j], up);
-        if (__any_sync(0xffffffffu, f[k] > 128.f)) {
-          const __nv_bfloat162 rest = __float2bfloat162_rn(f[k] > 128.f ? f[k] : 1.f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = __hmul2(o[j], rest);
-        }
-        const uint32_t* u = reinterpret_cast<const uint32_t*>(o);
-        *reinterpret_cast<uint4*>(dst + k * 1024 + write0) = make_uint4(u[0], u[1], u[2], u[3]);
-        *reinterpret_cast<uint4*>(dst + k * 1024 + write1) = make_uint4(u[4], u[5], u[6], u[7]);
+        const int slot = __shfl_sync(0xffffffffu, slots, step + (k >> 1));
+        // (without a condition, which would wait for the value here)
+        fresh_scale[k] = __ldg(reinterpret_cast<const float*>(
+            scales + int64_t(max(slot, 0) + r0 + 8 * (k & 1)) * kE4m3RowBytes));
       }
     }
-    if (!ok) break;
-    if (have && !rope) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (ld.el) mbar_arrive_cluster(ld.full + at * 8);
-      raw_phase ^= 1;
+    if (flying == 0) {
+      info[0] = word;
+      unit_slots[0] = slots;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) scale[0][k] = fresh_scale[k];
+    } else {
+      info[1] = word;
+      unit_slots[1] = slots;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) scale[1][k] = fresh_scale[k];
     }
-    if (!more) break;
-    have = true;
-    at = more_at;
-    at_wrap = more_wrap;
-    rope = more_rope;
-    held = slots;
-    first = fresh;
-    if (fresh) {
-      row0 = sg.r.q0 * a.H + sg.row0;
-      rows = sg.rows;
-      fresh = false;
-    }
+    ++flying;
   }
 }
 
 template <int kFmt>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThreads, 1)
-    chunk_kernel(const __grid_constant__ Maps maps, const Args a) {
+    chunk_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   using Lay = Layout<kFmt>;
   constexpr int kStages = Lay::kStages, kMmaWarp = Lay::kMmaWarp;
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -797,7 +801,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
   launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars->full[s], 2);
+      mbar_init(&bars->full[s], Lay::k8 ? 4 : 2);
       mbar_init(&bars->empty[0][s], 1);
       mbar_init(&bars->empty[1][s], 1);
     }
@@ -1305,7 +1309,7 @@ extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_
   } else {
     made = made &&
            make_map(&maps.k, a.cache + kE4m3Rope, num_slots, kE4m3RowBytes, 64, 1,
-                    std::min(page_size, 128), 1) &&
+                    std::min(page_size, 64), 1) &&
            make_map(&maps.code, cache, num_slots, kE4m3RowBytes, TS_D_LATENT, 1,
                     std::min(page_size, 64), 1, true);
     st = made ? launch_chunk<DSA_CACHE_E4M3>(maps, a, stream) : TS_ERR_CUDA;
