@@ -21,6 +21,7 @@
 // workspace, which chunk_merge_kernel joins in order (no atomics: results do
 // not depend on timing).
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -40,27 +41,30 @@ constexpr uint32_t kPBytes = 4 * kPBlock;        // 64 rows x 256 keys
 constexpr uint32_t kStageBytes = 16384;  // K: 128 keys x 64 dims; V: 64 keys x 2 x 64 dims
 constexpr uint32_t kVBox = 64 * 128;     // V: 64 keys x 64 dims
 constexpr uint32_t kBarBytes = 3072;
-constexpr int kSoftmaxWarps = 8;  // warps 0..7: two threads per TMEM lane
-// bf16 rows: warps 8..10 load by TMA (every third stage each), warp 11 issues
-// the products. 8-bit rows: warps 8..13 convert (every sixth half of a stage
-// each, two of them in flight), warp 14 loads Q, warp 15 issues the products.
-constexpr int kTmaWarps = 3, kConvertWarps = 6;
-constexpr uint32_t kRawHalf = 4096;  // 64 keys x 64 codes
+// Warp roles. bf16 rows: warps 0..7 softmax, 8..10 load by TMA (every third
+// stage each), 11 issues the products. 8-bit rows: warps 0..3 softmax, 4..13
+// convert (every tenth half of a stage each), 14 loads Q, 15 issues the
+// products: the conversion's integer instructions, not the softmax, are what
+// this kernel has most of.
+constexpr int kTmaWarps = 3, kConvertWarps = 10;
+constexpr uint32_t kRawUnit = 4096;  // 64 keys x 64 codes
 template <int kFmt>
 struct Layout {
   static constexpr bool k8 = kFmt == DSA_CACHE_E4M3;
+  static constexpr int kSoftmaxWarps = k8 ? 4 : 8;
+  static constexpr int kParts = kSoftmaxWarps / 4;  // threads of a TMEM lane
   static constexpr int kLoaders = k8 ? kConvertWarps + 1 : kTmaWarps;
   static constexpr int kMmaWarp = kSoftmaxWarps + kLoaders;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
   static constexpr int kStages = k8 ? 4 : 7;
-  static constexpr uint32_t kRawBytes = k8 ? 2 * kConvertWarps * kRawHalf : 0;
+  static constexpr uint32_t kRawBytes = k8 ? kConvertWarps * kRawUnit : 0;
   static constexpr uint32_t kSmem =
       kBarBytes + 1024 + kQBytes + kPBytes + kStages * kStageBytes + kRawBytes;
   static_assert(kSmem <= 227 * 1024, "dynamic shared memory of one CTA");
-  // Registers a thread after the split: the softmax's two warpgroups take what
-  // the others give back (of 384 x 168, or 512 x 128, at launch).
-  static constexpr int kSoftmaxRegs = k8 ? 136 : 200, kOtherRegs = k8 ? 120 : 104;
-  static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <=
+  // Registers a thread after the split: the softmax's warpgroups take what the
+  // others give back (of 384 x 168, or 512 x 128, at launch).
+  static constexpr int kSoftmaxRegs = k8 ? 224 : 200, kOtherRegs = k8 ? 96 : 104;
+  static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + (kThreads - 32 * kSoftmaxWarps) * kOtherRegs <=
                     kThreads * (k8 ? 128 : 168), "register split");
 };
 constexpr int kMaxStages = 7;
@@ -85,7 +89,7 @@ struct Bars {
   uint64_t s_full[2];       // both: a tile's scores are complete
   uint64_t p_full;          // even CTA: P written and S read in both CTAs
   uint64_t pv_done;         // both: a tile's value products are complete
-  uint64_t raw[kConvertWarps][2];  // a converting warp's units of codes
+  uint64_t raw[kConvertWarps];  // a converting warp's unit of codes
   uint64_t q_raw;                  // Q as loaded (8-bit rows: reordered before use)
   uint64_t drain;
   uint64_t sum[16];
@@ -93,7 +97,7 @@ struct Bars {
   int abort;
   int start_b, start_j, start_u;  // where the pair's stretch of work begins
   int64_t count;                  // and its length in units
-  float red[2][2][kRows];         // exchange between a row's four threads
+  float red[2][2][kRows];         // exchange between a row's threads
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
@@ -296,18 +300,19 @@ __device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, boo
 }
 
 // Barrier of the softmax warps (named barrier 1).
+template <int kThreads>
 __device__ __forceinline__ void softmax_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftmaxWarps) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
-
 // The same, and whether `ok` holds in every thread of them.
+template <int kThreads>
 __device__ __forceinline__ bool softmax_all(bool ok) {
   uint32_t all;
   asm volatile(
       "{\n .reg .pred p, r;\n setp.ne.u32 p, %1, 0;\n"
       " barrier.cta.red.and.pred r, 1, %2, p;\n selp.u32 %0, 1, 0, r;\n}"
       : "=r"(all)
-      : "r"(ok ? 1u : 0u), "n"(32 * kSoftmaxWarps)
+      : "r"(ok ? 1u : 0u), "n"(kThreads)
       : "memory");
   return all != 0;
 }
@@ -581,102 +586,131 @@ __device__ __forceinline__ void load_q_8bit(Loader& ld, Walk walk) {
 }
 
 // 8-bit rows: warp w of kConvertWarps. A stage is two units, its halves of 64
-// keys x 64 dims, dealt to the warps in turn; lane i takes row i / 4 of every
-// eight, and 16 of the 64 codes. Two units of a warp are in flight: their
-// codes (by TMA, into the warp's two raw spaces) and scales; a unit's space is
-// sent for again as soon as its codes are converted. A stage takes a warp some
-// 1500 clocks, so it is the units, not the stages, that are dealt: a place of
-// the ring is held that much shorter.
+// keys x 64 dims, dealt to the warps in turn; lane i takes the keys i and
+// i + 32. A unit's codes come by TMA (64-byte swizzle: the lanes' reads of one
+// piece of every row meet no bank twice) into the warp's raw space; once they
+// are in registers the next unit's are sent for, and land while this one is
+// converted. The integer pipe bounds this: some 230 of its instructions a unit
+// at half rate, 32 units a tile.
 __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
   constexpr int kStages = Layout<DSA_CACHE_E4M3>::kStages;
+  static_assert(kStages == 4, "a unit's place is (number / 2) % 4");
   static_assert((kConvertWarps + 1) / 2 <= 2 * kStages, "wait_free");
   const Args& a = ld.a;
   Bars* bars = ld.bars;
-  const int r0 = ld.lane >> 2, c = ld.lane & 3;
-  const uint32_t read = w * 2 * kRawHalf + r0 * 64 + c * 16;
-  const uint32_t write0 = r0 * 128 + (((2 * c) ^ r0) << 4);
-  const uint32_t write1 = r0 * 128 + (((2 * c + 1) ^ r0) << 4);
-  // a unit in flight: its keys of the context (bits 0..6), its valid 16-key
-  // steps (8..11), half (12), place (13..15), whether it is rope (16), whether
-  // Q comes before it (17), the place's use (18..); its slots; its scales
-  constexpr uint32_t kRope = 1u << 16, kFirst = 1u << 17;
-  uint32_t info[2];
-  int unit_slots[2];
-  float scale[2][8];
-  int flying = 0;       // units in flight: the older one is number 0
-  uint32_t units = 0, sent = 0, qn = 0;
-  // the walk over the stages
+  const int lane = ld.lane;
+  uint8_t* raw = ld.raw + w * kRawUnit;
+  uint64_t* raw_bar = &bars->raw[w];
+  const uint32_t read = lane * 64, read_x = (lane >> 1 & 3) << 4;
+  const uint32_t write = lane * 128, write_x = (lane & 7) << 4;
+  // the unit in flight: its number, its keys of the context, its valid 16-key
+  // steps, whether it is rope, whether Q comes before it; its slots; its scales
+  bool have = false, rope = false, first = false;
+  uint32_t number = 0, valid = 0;
+  int count = 0, unit_slots = -1;
+  float scale0 = 0.f, scale1 = 0.f;
+  uint32_t landed = 0, qn = 0;
+  // the walk: this warp's next unit is number i of the phase's n
   Segment sg;
-  bool inside = false, fresh = false, more_to_come = true;
-  int t = 0, i = 0, n = 0, here = -1, now = -1, next = -1, turn = 0;
-  uint32_t s = 0, wrap = 0;
+  bool inside = false, fresh = false, over = false;
+  int t = 0, i = w, n = 0, here = -1, now = -1, next = -1;
+  uint32_t next_number = w;
   for (;;) {
-    // this warp's next unit: 16-key steps step .. of `slots`, `left` keys of
-    // the context, block kb
-    bool more = false;
-    int slots = -1, step = 0, left = 0, kb = 0;
-    uint32_t word = 0;
-    while (!more && more_to_come) {
-      if (!inside) {
-        more_to_come = walk.next(a, sg);
-        if (!more_to_come) break;
-        inside = fresh = true;
-        t = sg.t0;
-        i = 0;
-        n = 2 * stages_of(sg, t);
-        here = -1;
-        now = ld.slots_of(sg, t);
-        next = ld.slots_of(sg, t + 1);
-        if (w == 0) {
-          ld.prefetch(now, kE4m3RowBytes);
-          ld.prefetch(next, kE4m3RowBytes);
-        }
-      }
-      for (; i < n && !more; ++i) {
-        const int h = i & 1;
-        if (turn == w) {
-          more = true;
-          int v = i >> 1;
-          word = h << 12 | s << 13 | wrap << 18 | (fresh ? kFirst : 0u);
-          if (t < sg.t1 && v < kBlocks) {
-            slots = now;
-            step = ld.rank * 8 + h * 4;
-            left = sg.r.ctx - t * kKeys - int(ld.rank) * 128 - h * 64;
-            kb = v;
-            if (v == kBlocks - 1) word |= kRope;
-          } else {
-            v -= t < sg.t1 ? kBlocks : 0;  // 64-key group v / 2, dims half v % 2
-            slots = here;
-            step = (v >> 1) * 4;
-            left = sg.r.ctx - (t - 1) * kKeys - (v >> 1) * 64;
-            kb = ld.rank * 4 + (v & 1) * 2 + h;
-          }
-          fresh = false;
-        }
-        if (++turn == kConvertWarps) turn = 0;
-        if (h && ++s == kStages) s = 0, ++wrap;
-      }
-      if (!more) {  // the phase is through
+    while (!over && i >= n) {  // on to the phase that holds the next unit
+      i -= n;
+      if (inside) {
         here = now;
         now = next;
         inside = ++t <= sg.t1;
-        if (inside) {
-          i = 0;
-          n = 2 * stages_of(sg, t);
-          next = ld.slots_of(sg, t + 1);
-          if (w == 0) ld.prefetch(next, kE4m3RowBytes);
-        }
+      }
+      if (!inside) {
+        over = !walk.next(a, sg);
+        if (over) break;
+        inside = fresh = true;
+        t = sg.t0;
+        here = -1;
+        now = ld.slots_of(sg, t);
+        if (w == 0) ld.prefetch(now, kE4m3RowBytes);
+      }
+      n = 2 * stages_of(sg, t);
+      next = ld.slots_of(sg, t + 1);
+      if (w == 0) ld.prefetch(next, kE4m3RowBytes);
+    }
+    if (over && !have) break;
+
+    // the unit in flight: its codes into registers
+    uint4 code[8];
+    float f0 = scale0, f1 = scale1;
+    if (have && !rope) {
+      if (!ld.wait(raw_bar, landed & 1)) break;
+      ++landed;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        code[k] = *reinterpret_cast<const uint4*>(raw + read + (k >> 2) * 2048 +
+                                                  (((k & 3) << 4) ^ read_x));
+      if (count < 64 || valid != 15) {
+        // keys that are not the request's: codes of 0 and a scale that is no NaN
+        const bool in0 = lane < count && (valid >> (lane >> 4) & 1);
+        const bool in1 = lane + 32 < count && (valid >> (2 + (lane >> 4)) & 1);
+        f0 = in0 ? f0 : 0.f;
+        f1 = in1 ? f1 : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (!(k < 4 ? in0 : in1)) code[k] = make_uint4(0, 0, 0, 0);
       }
     }
-    if (flying == 0 && !more) break;
+    __syncwarp();
 
-    // convert the older unit, once two are in flight or none follows
-    if (flying == 2 || !more) {
-      const uint32_t at = info[0] >> 13 & 7, half = info[0] >> 12 & 1;
-      if (info[0] & kFirst) {  // Q's latent part into the codes' order
+    // the next one's sent for
+    bool next_rope = false;
+    uint32_t next_valid = 0;
+    int next_count = 0, slots = -1;
+    if (!over) {
+      int v = i >> 1, step, kb;
+      if (t < sg.t1 && v < kBlocks) {
+        slots = now;
+        step = ld.rank * 8 + (i & 1) * 4;
+        next_count = sg.r.ctx - t * kKeys - int(ld.rank) * 128 - (i & 1) * 64;
+        kb = v;
+        next_rope = v == kBlocks - 1;
+      } else {
+        v -= t < sg.t1 ? kBlocks : 0;  // 64-key group v / 2, dims half v % 2
+        slots = here;
+        step = (v >> 1) * 4;
+        next_count = sg.r.ctx - (t - 1) * kKeys - (v >> 1) * 64;
+        kb = ld.rank * 4 + (v & 1) * 2 + (i & 1);
+      }
+      next_count = min(max(next_count, 0), 64);
+      next_valid = __ballot_sync(0xffffffffu, slots >= 0) >> step & 15;
+      // (from here on lanes 0..3 hold the unit's slots)
+      slots = __shfl_sync(0xffffffffu, slots, (step + lane) & 31);
+      if (!next_rope) {
+        const uint32_t boxes = next_valid & (ld.v_step == 4 ? 1u : ld.v_step == 2 ? 5u : 15u);
+        if (ld.el) {
+          if (boxes) mbar_expect_tx(raw_bar, __popc(boxes) * ld.v_step * 1024);
+          else mbar_arrive(raw_bar);
+        }
+        for (int k = 0; k < 4; k += ld.v_step) {
+          const int slot = __shfl_sync(0xffffffffu, slots, k);
+          if (slot >= 0 && ld.el)
+            tma_load_3d(raw + k * 1024, &ld.maps.code, raw_bar, kb * 64, slot, 0);
+        }
+        // (without a condition, which would wait for the values here)
+        const int slot0 = max(__shfl_sync(0xffffffffu, slots, lane >> 4), 0) + (lane & 15);
+        const int slot1 = max(__shfl_sync(0xffffffffu, slots, 2 + (lane >> 4)), 0) + (lane & 15);
+        const uint8_t* scales = a.cache + TS_D_LATENT + (kb >> 1) * 4;
+        scale0 = __ldg(reinterpret_cast<const float*>(scales + int64_t(slot0) * kE4m3RowBytes));
+        scale1 = __ldg(reinterpret_cast<const float*>(scales + int64_t(slot1) * kE4m3RowBytes));
+      }
+    }
+
+    // the unit in flight: into its place
+    if (have) {
+      const uint32_t at = number >> 1 & 3, half = number & 1, bar = ld.full + at * 8;
+      if (first) {  // Q's latent part into the codes' order
         if (!ld.wait(&bars->q_raw, qn & 1)) break;
         ++qn;
-        for (int k = w * 32 + ld.lane; k < kRowsCta * 64; k += kConvertWarps * 32) {
+        for (int k = w * 32 + lane; k < kRowsCta * 64; k += kConvertWarps * 32) {
           uint4* x = reinterpret_cast<uint4*>(ld.q_tile) + k;
           *x = code_order(*x);
         }
@@ -684,100 +718,46 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
         __syncwarp();
         if (ld.el) mbar_arrive_cluster(ld.q_full);
       }
-      if (!ld.wait_free(at, info[0] >> 18)) break;
+      if (!ld.wait_free(at, number >> 3)) break;
       uint8_t* dst = ld.ring + at * kStageBytes + half * kVBox;
-      const uint32_t bar = ld.full + at * 8, valid = info[0] >> 8 & 15;
-      if (info[0] & kRope) {  // bf16 as it is, by TMA
+      if (rope) {  // bf16 as it is, by TMA
         const uint32_t boxes = valid & (ld.v_step == 4 ? 1u : ld.v_step == 2 ? 5u : 15u);
         if (ld.el) mbar_expect_tx_cluster(bar, __popc(boxes) * ld.v_step * 2048);
         for (int k = 0; k < 4; k += ld.v_step) {
-          const int slot = __shfl_sync(0xffffffffu, unit_slots[0], ld.rank * 8 + half * 4 + k);
+          const int slot = __shfl_sync(0xffffffffu, unit_slots, k);
           if (slot >= 0 && ld.el) tma_load_3d_pair(dst + k * 2048, &ld.maps.k, bar, 0, slot, 0);
         }
       } else {
-        const uint32_t space = units & 1;
-        if (!ld.wait(&bars->raw[w][space], units >> 1 & 1)) break;
-        ++units;
-        const uint8_t* src = ld.raw + read + space * kRawHalf;
-        const int count = info[0] & 0x7f;
-        const bool whole = count == 64 && valid == 15;
-        float top = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          // keys that are not the request's: codes of 0 and a scale that is no NaN
-          if (!whole && !(r0 + 8 * k < count && (valid >> (k >> 1) & 1))) scale[0][k] = 0.f;
-          top = fmaxf(top, scale[0][k]);
-        }
         // 2^120 scale is past bf16's range for a scale above 2^7
-        const bool big = __any_sync(0xffffffffu, top > 128.f);
+        const bool big = __any_sync(0xffffffffu, fmaxf(f0, f1) > 128.f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          uint4 code = *reinterpret_cast<const uint4*>(src + k * 512);
-          if (!whole && scale[0][k] == 0.f) code = make_uint4(0, 0, 0, 0);
+          const float f = k < 4 ? f0 : f1;
           uint4 o[2];
-          widen_codes(code, big ? 0x1p120f : scale[0][k] * 0x1p120f, o);
+          widen_codes(code[k], big ? 0x1p120f : f * 0x1p120f, o);
           if (big) {
-            o[0] = scaled(o[0], scale[0][k]);
-            o[1] = scaled(o[1], scale[0][k]);
+            o[0] = scaled(o[0], f);
+            o[1] = scaled(o[1], f);
           }
-          *reinterpret_cast<uint4*>(dst + k * 1024 + write0) = o[0];
-          *reinterpret_cast<uint4*>(dst + k * 1024 + write1) = o[1];
+          uint8_t* row = dst + write + (k >> 2) * 4096;
+          *reinterpret_cast<uint4*>(row + (((k & 3) << 5) ^ write_x)) = o[0];
+          *reinterpret_cast<uint4*>(row + ((((k & 3) << 5) + 16) ^ write_x)) = o[1];
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (ld.el) mbar_arrive_cluster(bar);
       }
-      --flying;
-      info[0] = info[1];
-      unit_slots[0] = unit_slots[1];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) scale[0][k] = scale[1][k];
     }
-    if (!more) continue;
-
-    // send for the new one
-    uint32_t valid = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      valid |= (__shfl_sync(0xffffffffu, slots, step + k) >= 0 ? 1u : 0u) << k;
-    word |= static_cast<uint32_t>(min(max(left, 0), 64)) | valid << 8;
-    float fresh_scale[8];
-    if (!(word & kRope)) {
-      const uint32_t space = sent & 1;
-      ++sent;
-      uint64_t* bar = &bars->raw[w][space];
-      const uint32_t boxes = valid & (ld.v_step == 4 ? 1u : ld.v_step == 2 ? 5u : 15u);
-      if (ld.el) {
-        if (boxes) mbar_expect_tx(bar, __popc(boxes) * ld.v_step * 1024);
-        else mbar_arrive(bar);
-      }
-      for (int k = 0; k < 4; k += ld.v_step) {
-        const int slot = __shfl_sync(0xffffffffu, slots, step + k);
-        if (slot >= 0 && ld.el)
-          tma_load_3d(ld.raw + (w * 2 + space) * kRawHalf + k * 1024, &ld.maps.code, bar, kb * 64,
-                      slot, 0);
-      }
-      const uint8_t* scales = a.cache + TS_D_LATENT + (kb >> 1) * 4;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int slot = __shfl_sync(0xffffffffu, slots, step + (k >> 1));
-        // (without a condition, which would wait for the value here)
-        fresh_scale[k] = __ldg(reinterpret_cast<const float*>(
-            scales + int64_t(max(slot, 0) + r0 + 8 * (k & 1)) * kE4m3RowBytes));
-      }
-    }
-    if (flying == 0) {
-      info[0] = word;
-      unit_slots[0] = slots;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) scale[0][k] = fresh_scale[k];
-    } else {
-      info[1] = word;
-      unit_slots[1] = slots;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) scale[1][k] = fresh_scale[k];
-    }
-    ++flying;
+    have = !over;
+    rope = next_rope;
+    first = fresh;
+    fresh = false;
+    number = next_number;
+    valid = next_valid;
+    count = next_count;
+    unit_slots = slots;
+    next_number += kConvertWarps;
+    i += kConvertWarps;
   }
 }
 
@@ -786,6 +766,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
     chunk_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   using Lay = Layout<kFmt>;
   constexpr int kStages = Lay::kStages, kMmaWarp = Lay::kMmaWarp;
+  constexpr int kSoftmaxWarps = Lay::kSoftmaxWarps, kParts = Lay::kParts;
+  constexpr int kCols = 128 / kParts;  // score columns of a softmax thread
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Bars* bars = reinterpret_cast<Bars*>(smem_raw);
   uint8_t* q_tile = reinterpret_cast<uint8_t*>(
@@ -809,9 +791,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->s_full[0], 1);
     mbar_init(&bars->s_full[1], 1);
-    mbar_init(&bars->p_full, 2 * kSoftmaxWarps);
+    mbar_init(&bars->p_full, 2 * Lay::kSoftmaxWarps);
     mbar_init(&bars->pv_done, 1);
-    for (int i = 0; i < 2 * kConvertWarps; ++i) mbar_init(&bars->raw[i >> 1][i & 1], 1);
+    for (int i = 0; i < kConvertWarps; ++i) mbar_init(&bars->raw[i], 1);
     mbar_init(&bars->q_raw, 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
@@ -831,9 +813,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
   Walk walk(bars);
   Segment sg;
   if (warp < kSoftmaxWarps) {
-    // ---------------- softmax and epilogue: two threads per TMEM lane ----------------
+    // ---------------- softmax and epilogue: kParts threads per TMEM lane ----------------
     // Lanes r and r + 64 hold row r: of S keys 0..127 and 128..255, of O dims
-    // 0..255 and 256..511; of either, a lane's two threads take half the columns.
+    // 0..255 and 256..511; of either, a lane's threads take equal parts of the
+    // columns.
     regs_inc<Lay::kSoftmaxRegs>();
     const int L = (warp & 3) * 32 + lane, r = L & 63, half = L >> 6, part = warp >> 2;
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -847,70 +830,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
       int limit = 0;
       if (rr < sg.rows)
         limit = a.causal ? max(0, sg.r.ctx - sg.r.n + (sg.row0 + rr) / a.H + 1) : sg.r.ctx;
-      float m = -INFINITY, l = 0.f;
+      // (the sum in parts of 64 columns, whatever the threads: both formats then
+      // add in one order, and equal rows give equal results)
+      float m = -INFINITY, l64[kCols / 64] = {};
       for (int t = sg.t0; t < sg.t1; ++t, ++tg) {
-        const uint32_t ts = trow + (tg & 1) * 128 + part * 64;
-        const int nv = min(max(limit - t * kKeys - half * 128 - part * 64, 0), 64);
-        const bool whole = __all_sync(0xffffffffu, nv == 64);
+        const uint32_t ts = trow + (tg & 1) * 128 + part * kCols;
+        const int nv = min(max(limit - t * kKeys - half * 128 - part * kCols, 0), kCols);
+        const bool whole = __all_sync(0xffffffffu, nv == kCols);
         if (ok) ok = mbar_warp_wait<false>(&bars->s_full[tg & 1], (tg >> 1) & 1, abort, wait_ns);
-        // the thread's 64 scores, once, into registers
-        uint32_t x[2][32];
+        // the thread's scores, once, into registers
+        uint32_t x[kCols / 32][32];
         float mx = -INFINITY;
         if (ok) {
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) tmem_ld32(ts + 32 * c, x[c]);
+          for (int c = 0; c < kCols / 32; ++c) tmem_ld32(ts + 32 * c, x[c]);
           tmem_wait_ld();
           if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
+            for (int i = 0; i < kCols; ++i)
               if (i >= nv) x[i >> 5][i & 31] = __float_as_uint(-INFINITY);
           }
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 64; i += 2)
+          for (int i = 0; i < kCols; i += 2)
             m4[(i >> 1) & 3] =
                 fmaxf(fmaxf(m4[(i >> 1) & 3], __uint_as_float(x[i >> 5][i & 31])),
                       __uint_as_float(x[i >> 5][(i & 31) + 1]));
           mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          // (minus infinity times a scale of 0 is no number)
-          mx = mx == -INFINITY ? mx : mx * a.scale_log2;
+          mx *= a.scale_log2;
         }
         bars->red[tg & 1][part][L] = mx;
-        softmax_sync();
+        softmax_sync<32 * Lay::kSoftmaxWarps>();
         {
           const auto& e = bars->red[tg & 1];
-          mx = fmaxf(fmaxf(e[0][r], e[1][r]), fmaxf(e[0][r + 64], e[1][r + 64]));
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) mx = fmaxf(mx, fmaxf(e[k][r], e[k][r + 64]));
         }
         const bool moves = mx > m + kSlack;
         const float f = moves ? fast_exp2(m - mx) : 1.f;
         if (moves) m = mx;
-        l *= f;
-        const float mu = m == -INFINITY ? 0.f : m;
-        uint32_t packed[32];
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float p0 = fast_exp2(fmaf(__uint_as_float(x[i >> 4][(2 * i) & 31]), a.scale_log2, -mu));
-          float p1 =
+        for (int k = 0; k < kCols / 64; ++k) l64[k] *= f;
+        const float mu = m == -INFINITY ? 0.f : m;
+        uint32_t packed[kCols / 2];
+        float l4[kCols / 64][4] = {};
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i) {
+          const float p0 =
+              fast_exp2(fmaf(__uint_as_float(x[i >> 4][(2 * i) & 31]), a.scale_log2, -mu));
+          const float p1 =
               fast_exp2(fmaf(__uint_as_float(x[i >> 4][(2 * i + 1) & 31]), a.scale_log2, -mu));
-          if (!whole) {
-            p0 = 2 * i < nv ? p0 : 0.f;
-            p1 = 2 * i + 1 < nv ? p1 : 0.f;
-          }
-          l4[(2 * i) & 3] += p0;
-          l4[(2 * i + 1) & 3] += p1;
+          l4[i / 32][(2 * i) & 3] += p0;
+          l4[i / 32][(2 * i + 1) & 3] += p1;
           const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
           packed[i] = *reinterpret_cast<const uint32_t*>(&h2);
         }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+#pragma unroll
+        for (int k = 0; k < kCols / 64; ++k)
+          l64[k] += (l4[k][0] + l4[k][1]) + (l4[k][2] + l4[k][3]);
         // the tile before this one is in O, and its P read
         if (ok && tg > 0) ok = mbar_warp_wait<false>(&bars->pv_done, (tg - 1) & 1, abort, wait_ns);
         if (!ok) continue;  // the barrier above stays matched in every warp
         if (t > sg.t0 && __any_sync(0xffffffffu, moves)) {
           tc_fence_after();
           uint32_t v[32];
-          for (int c = part * 128; c < part * 128 + 128; c += 32) {
+#pragma unroll 1
+          for (int c = part * (256 / kParts); c < (part + 1) * (256 / kParts); c += 32) {
             tmem_ld32(trow + kOCol + c, v);
             tmem_wait_ld();
 #pragma unroll
@@ -919,10 +905,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
           }
           tmem_wait_st();
         }
-        uint8_t* prow = p_tile + (half * 2 + part) * kPBlock + r * 128;
+        uint8_t* prow = p_tile + (half * 2 + part * (kCols / 64)) * kPBlock + r * 128;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(prow + ((j ^ (r & 7)) << 4)) =
+        for (int j = 0; j < kCols / 8; ++j)
+          *reinterpret_cast<uint4*>(prow + (j >> 3) * kPBlock + (((j & 7) ^ (r & 7)) << 4)) =
               make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
@@ -931,14 +917,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
       }
       // the row tile's sums: O from TMEM, normalised into the output or raw
       // into the workspace
-      bars->red[tg & 1][part][L] = l;
-      softmax_sync();
+#pragma unroll
+      for (int k = 0; k < kCols / 64; ++k) bars->red[tg & 1][part + k][L] = l64[k];
+      softmax_sync<32 * Lay::kSoftmaxWarps>();
+      float l;
       {
         const auto& e = bars->red[tg & 1];
-        l = (e[0][r] + e[1][r]) + (e[0][r + 64] + e[1][r + 64]);
+        l = (e[0][r] + e[0][r + 64]) + (e[1][r] + e[1][r + 64]);
       }
       if (ok) ok = mbar_warp_wait<false>(&bars->pv_done, (tg - 1) & 1, abort, wait_ns);
-      ok = softmax_all(ok);  // the same in every warp: all go on, or none
+      ok = softmax_all<32 * Lay::kSoftmaxWarps>(ok);  // the same in every warp: all go on, or none
       if (!ok) break;
       tc_fence_after();
       const int64_t grow = int64_t(sg.r.q0) * a.H + sg.row0 + rr;  // output row
@@ -947,7 +935,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
         const float inv = l > 0.f ? 1.f / l : 0.f;
         uint4* dst = reinterpret_cast<uint4*>(a.out + grow * DSA_DV + half * 256);
         uint32_t v[32];
-        for (int c = part * 128; c < part * 128 + 128; c += 32) {
+#pragma unroll 1
+        for (int c = part * (256 / kParts); c < (part + 1) * (256 / kParts); c += 32) {
           tmem_ld32(trow + kOCol + c, v);
           tmem_wait_ld();
           natural_order<kFmt>(v);
@@ -972,7 +961,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
         const int64_t prow = int64_t(slot) * a.part_rows + rr;
         float4* dst = reinterpret_cast<float4*>(a.opart + prow * DSA_DV + half * 256);
         uint32_t v[32];
-        for (int c = part * 128; c < part * 128 + 128; c += 32) {
+#pragma unroll 1
+        for (int c = part * (256 / kParts); c < (part + 1) * (256 / kParts); c += 32) {
           tmem_ld32(trow + kOCol + c, v);
           tmem_wait_ld();
           natural_order<kFmt>(v);
@@ -1206,8 +1196,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Arg
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // 3-D map over rows of `blocks` blocks of `inner` values: dims {inner, rows,
-// blocks}; box {64, box_rows, box_blocks}. bf16 values, swizzled by 128 bytes,
-// or (codes) plain bytes.
+// blocks}; box {64, box_rows, box_blocks}. bf16 values swizzled by 128 bytes, or
+// (codes) bytes swizzled by 64.
 bool make_map(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_bytes,
               uint64_t inner, uint64_t blocks, uint32_t box_rows, uint32_t box_blocks,
               bool codes = false) {
@@ -1219,7 +1209,7 @@ bool make_map(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_byt
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
              const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             codes ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1281,7 +1271,8 @@ extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_
   a.page_shift = __builtin_ctz(page_size);
   a.ctx_len = ctx_len;
   a.causal = causal;
-  a.scale_log2 = std::fabs(scale) * kLog2e;
+  // (above 0: a masked score, minus infinity, times 0 would be no number)
+  a.scale_log2 = std::max(std::fabs(scale) * kLog2e, FLT_MIN);
   a.negate = scale < 0.f;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
