@@ -80,48 +80,69 @@ __global__ void __launch_bounds__(kThreads)
   if (lane < 8) reinterpret_cast<uint4*>(dst + kE4m3Rope)[lane] = r;
 }
 
-// One warp a row.
-template <int kFmt>
+// kReadRows rows a warp: their positions and pages are looked up by as many
+// lanes at once, and every row's pieces are on their way before the first is
+// stored. Four rows a warp where there are rows for every SM, else one
+// (measured, 8-bit rows: 65,536 rows 30.9 us with one and 25.4 with four, 256
+// rows 4.3 and 6.2).
+template <int kFmt, int kReadRows>
 __global__ void __launch_bounds__(kThreads)
     cache_read_kernel(const uint8_t* __restrict__ cache, int64_t num_slots,
                       const int32_t* __restrict__ block_table, int64_t table_stride,
                       int page_shift, const int32_t* __restrict__ pos,
                       const int32_t* __restrict__ ctx_len, int64_t rows, int k,
                       uint8_t* __restrict__ sel, int32_t* err) {
-  const int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t row0 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kReadRows;
   const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const int b = static_cast<int>(row / k);
-  const int32_t t = __ldg(pos + row);
-  if (t < 0 || t >= __ldg(ctx_len + b)) {
-    if (lane == 0) report(err, TS_DEVERR_ID_RANGE);
-    return;
+  int32_t slot = -1;
+  if (lane < kReadRows && row0 + lane < rows) {
+    const int b = static_cast<int>((row0 + lane) / k);
+    const int32_t t = __ldg(pos + row0 + lane);
+    if (t < 0 || t >= __ldg(ctx_len + b)) {
+      report(err, TS_DEVERR_ID_RANGE);
+    } else {
+      const int page_i = t >> page_shift;
+      int64_t at = -1;
+      if (page_i < table_stride)
+        at = (int64_t(__ldg(block_table + b * table_stride + page_i)) << page_shift) +
+             (t & ((1 << page_shift) - 1));
+      if (at < 0 || at >= num_slots) report(err, TS_DEVERR_SLOT_RANGE);
+      else slot = static_cast<int32_t>(at);
+    }
   }
-  const int page_i = t >> page_shift;
-  int64_t slot = -1;
-  if (page_i < table_stride)
-    slot = (int64_t(__ldg(block_table + b * table_stride + page_i)) << page_shift) +
-           (t & ((1 << page_shift) - 1));
-  if (slot < 0 || slot >= num_slots) {
-    if (lane == 0) report(err, TS_DEVERR_SLOT_RANGE);
-    return;
-  }
-  const uint8_t* src = cache + slot * cache_row_bytes(kFmt);
-  uint4* dst = reinterpret_cast<uint4*>(sel + row * DSA_ROW_BYTES);
-  if (kFmt == DSA_CACHE_BF16) {
+  uint4 x[kReadRows][kFmt == DSA_CACHE_BF16 ? 3 : 2];
+  float scale[kReadRows];
+#pragma unroll
+  for (int i = 0; i < kReadRows; ++i) {
+    const int32_t at = __shfl_sync(0xffffffffu, slot, i);
+    if (at < 0) continue;
+    const uint8_t* src = cache + int64_t(at) * cache_row_bytes(kFmt);
     const uint4* s = reinterpret_cast<const uint4*>(src);
-    dst[lane] = __ldg(s + lane);
-    dst[lane + 32] = __ldg(s + lane + 32);
-    if (lane < 8) dst[64 + lane] = __ldg(s + 64 + lane);
-    return;
+    x[i][0] = __ldg(s + lane);
+    if (kFmt == DSA_CACHE_BF16) {
+      x[i][1] = __ldg(s + lane + 32);
+      if (lane < 8) x[i][2] = __ldg(s + 64 + lane);
+    } else {
+      scale[i] = __ldg(reinterpret_cast<const float*>(src + TS_D_LATENT) + (lane >> 3));
+      if (lane < 8) x[i][1] = __ldg(reinterpret_cast<const uint4*>(src + kE4m3Rope) + lane);
+    }
   }
-  const uint4 c = __ldg(reinterpret_cast<const uint4*>(src) + lane);
-  const float s = __ldg(reinterpret_cast<const float*>(src + TS_D_LATENT) + (lane >> 3));
-  uint4 o[2];
-  e4m3x16_to_bf16(c, s, o);
-  dst[2 * lane] = o[0];
-  dst[2 * lane + 1] = o[1];
-  if (lane < 8) dst[64 + lane] = __ldg(reinterpret_cast<const uint4*>(src + kE4m3Rope) + lane);
+#pragma unroll
+  for (int i = 0; i < kReadRows; ++i) {
+    if (__shfl_sync(0xffffffffu, slot, i) < 0) continue;
+    uint4* dst = reinterpret_cast<uint4*>(sel + (row0 + i) * DSA_ROW_BYTES);
+    if (kFmt == DSA_CACHE_BF16) {
+      dst[lane] = x[i][0];
+      dst[lane + 32] = x[i][1];
+      if (lane < 8) dst[64 + lane] = x[i][2];
+    } else {
+      uint4 o[2];
+      e4m3x16_to_bf16(x[i][0], scale[i], o);
+      dst[2 * lane] = o[0];
+      dst[2 * lane + 1] = o[1];
+      if (lane < 8) dst[64 + lane] = x[i][1];
+    }
+  }
 }
 
 }  // namespace
@@ -183,16 +204,22 @@ extern "C" ts_status dsa_cache_read(const void* cache, int64_t num_slots, int fm
   if (st != TS_OK) return st;
   if (!pos || !ctx_len || !sel || !aligned16(sel) || B <= 0 || k <= 0) return TS_ERR_INVALID_ARG;
   const int64_t rows = int64_t(B) * k;
-  if (rows > INT_MAX) return TS_ERR_UNSUPPORTED;
+  if (rows > INT_MAX || num_slots > INT_MAX) return TS_ERR_UNSUPPORTED;
   const auto* c = static_cast<const uint8_t*>(cache);
   auto* o = static_cast<uint8_t*>(sel);
   const int shift = __builtin_ctz(page_size);
-  const unsigned grid = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
-  if (fmt == DSA_CACHE_BF16)
-    cache_read_kernel<DSA_CACHE_BF16><<<grid, kThreads, 0, stream>>>(
-        c, num_slots, block_table, table_stride, shift, pos, ctx_len, rows, k, o, err);
-  else
-    cache_read_kernel<DSA_CACHE_E4M3><<<grid, kThreads, 0, stream>>>(
-        c, num_slots, block_table, table_stride, shift, pos, ctx_len, rows, k, o, err);
+  auto launch = [&](auto kernel, int rows_warp) {
+    const unsigned grid = static_cast<unsigned>((rows + kWarps * rows_warp - 1) / (kWarps * rows_warp));
+    kernel<<<grid, kThreads, 0, stream>>>(c, num_slots, block_table, table_stride, shift, pos,
+                                          ctx_len, rows, k, o, err);
+  };
+  const bool many = rows >= int64_t(sm_count()) * kWarps * 8;  // a full SM's warps
+  if (fmt == DSA_CACHE_BF16) {
+    if (many) launch(cache_read_kernel<DSA_CACHE_BF16, 4>, 4);
+    else launch(cache_read_kernel<DSA_CACHE_BF16, 1>, 1);
+  } else {
+    if (many) launch(cache_read_kernel<DSA_CACHE_E4M3, 4>, 4);
+    else launch(cache_read_kernel<DSA_CACHE_E4M3, 1>, 1);
+  }
   return launch_status();
 }

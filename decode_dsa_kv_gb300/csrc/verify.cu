@@ -12,7 +12,11 @@
 // The weights are whole multiples of 2^-60 in 64 bits: sums are exact, so the
 // drawn token depends neither on the split nor on the order, and an integer
 // add costs a fraction of an FP64 one here. (An fp32 running sum over 10^5
-// tokens would move the borders between tokens by about 1e-6.)
+// tokens would move the borders between tokens by about 1e-6.) A probability
+// is cut into three whole numbers by additions rounded towards zero, on the
+// full-rate fp32 pipe: shifting its mantissa into 64 bits takes some 12
+// half-rate integer instructions a value instead, and was what bounded the
+// pass (128 requests x 131,072 tokens: 86 us).
 #include "common.cuh"
 
 namespace dsakv {
@@ -22,7 +26,7 @@ constexpr int kThreads = 512;
 constexpr int kPer = 8;                 // tokens of a tile per thread
 constexpr int kTile = kThreads * kPer;  // 4096
 constexpr int kMaxCluster = 8;
-constexpr int kMaxV = 1 << 26;
+constexpr int kMaxV = 1 << 23;  // 256 tiles a CTA: 34 KB of sums
 constexpr int kFrac = 60;
 
 // p in [0, 2) as a multiple of 2^-60 (smaller parts are cut off: below 2^-36
@@ -37,6 +41,37 @@ __device__ __forceinline__ uint64_t fixed(float p, int* bad) {
   const int sh = static_cast<int>(b >> 23) - (150 - kFrac);
   const uint64_t m = (b >> 23) ? ((b & 0x7fffffu) | 0x800000u) : 0u;  // subnormals: below 2^-126
   return sh >= 0 ? m << sh : (sh > -24 ? m >> -sh : 0);
+}
+
+// floor(p 2^60) = H 2^39 + L 2^17 + M of p in [0, 2), each as the bits of a
+// float 4 + x: 4 + p rounded down is 4 + H 2^-21; what that leaves, times 2^22,
+// gives L in the same way, and its rest, times 2^17, M. For two values at
+// once (packed fp32), of which the numbers' differences come back: the 4's
+// bits cancel.
+struct Parts {
+  int32_t h, l, m;
+};
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ int32_t bits_apart(uint64_t v) {
+  return static_cast<int32_t>(static_cast<uint32_t>(v) - static_cast<uint32_t>(v >> 32));
+}
+__device__ __forceinline__ Parts parts_apart(float p, float q) {
+  const uint64_t x = pack2(p, q), four = pack2(4.f, 4.f), minus4 = pack2(-4.f, -4.f),
+                 one = pack2(-1.f, -1.f), up22 = pack2(0x1p22f, 0x1p22f),
+                 up17 = pack2(0x1p17f, 0x1p17f);
+  uint64_t a, b, c, t, r, s;
+  asm("add.rz.f32x2 %0, %1, %2;" : "=l"(a) : "l"(x), "l"(four));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(a), "l"(minus4));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(t), "l"(one), "l"(x));  // exact: < 2^-21
+  asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(b) : "l"(r), "l"(up22), "l"(four));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(b), "l"(one), "l"(four));  // 4 - b, exact
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(s) : "l"(r), "l"(up22), "l"(t));    // exact: < 2^-21
+  asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(c) : "l"(s), "l"(up17), "l"(four));
+  return {bits_apart(a), bits_apart(b), bits_apart(c)};
 }
 
 // u in [0, 1) as a multiple of 2^-64; outside it the nearest end.
@@ -64,6 +99,37 @@ struct Weights {
     }
     return t == hot ? 0 : a;
   }
+  // This thread's tokens of a tile: t, t + kThreads, ..
+  struct Tile {
+    float a[kPer], b[kPer];
+  };
+  __device__ __forceinline__ void load(Tile& x, int64_t t, int V) const {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int64_t k = t + j * kThreads;
+      x.a[j] = k < V ? __ldg(p + k) : 0.f;
+      x.b[j] = q && !plain && k < V ? __ldg(q + k) : 0.f;
+    }
+  }
+  // The warp's share of the tile's sum, in every lane; exact as long as *top
+  // (the largest bits) stays below those of 2.
+  __device__ __forceinline__ uint64_t warp_tile_sum(const Tile& x, int64_t t, uint32_t* top) const {
+    int32_t h = 0, l = 0, m = 0;  // |each| below kPer 2^22, the warp's below 2^30
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      *top = max(*top, max(__float_as_uint(x.a[j]), __float_as_uint(x.b[j])));
+      const Parts u = parts_apart(x.a[j], x.b[j]);
+      if (x.a[j] > x.b[j] && (plain || t + j * kThreads != hot)) {
+        h += u.h;
+        l += u.l;
+        m += u.m;
+      }
+    }
+    h = __reduce_add_sync(0xffffffffu, h);
+    l = __reduce_add_sync(0xffffffffu, l);
+    m = __reduce_add_sync(0xffffffffu, m);
+    return (int64_t(h) << 39) + (int64_t(l) << 17) + m;
+  }
 };
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
@@ -78,13 +144,14 @@ __device__ __forceinline__ uint64_t ld_dsmem_u64(uint32_t addr) {
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     verify_kernel(const int32_t* __restrict__ drafts, const int32_t* __restrict__ n_draft,
                   const float* __restrict__ target, int64_t target_stride,
                   const float* __restrict__ draft, int64_t draft_stride,
                   const float* __restrict__ u, int n, int V, int cluster, int tiles_per_cta,
                   int32_t* __restrict__ tokens, int32_t* __restrict__ accepted, int32_t* err) {
-  extern __shared__ uint64_t tile_sum[];  // this CTA's tiles
+  extern __shared__ uint64_t tile_sum[];  // this CTA's tiles, then their warps' parts
+  uint64_t* part = tile_sum + tiles_per_cta;
   __shared__ uint64_t cta_sum;
   __shared__ uint64_t warp_part[kThreads / 32];
   __shared__ int first_refused;
@@ -125,26 +192,40 @@ __global__ void __launch_bounds__(kThreads)
   const int tile0 = rank * tiles_per_cta;
   int next = -1;
   for (int pass = 0; pass < 2; ++pass) {
-    uint64_t mine = 0;
+    // every warp's part of every tile's sum; the tiles' sums follow
+    uint32_t top = 0;  // the largest bits seen: 2 and more, NaN or a sign
+    Weights::Tile ahead;
+    w.load(ahead, int64_t(tile0) * kTile + tid, V);
     for (int i = 0; i < tiles_per_cta; ++i) {
-      const int64_t t0 = int64_t(tile0 + i) * kTile;
-      uint64_t s = 0;
-      if (t0 < V) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) s += w.at(static_cast<int>(t0) + j * kThreads + tid, V, &bad);
-      }
-      s = warp_sum(s);
-      __syncthreads();
-      if (lane == 0) warp_part[warp] = s;
-      __syncthreads();
-      if (tid == 0) {
-        uint64_t v = 0;
-        for (int k = 0; k < kThreads / 32; ++k) v += warp_part[k];
-        tile_sum[i] = v;
-        mine += v;
-      }
+      const int64_t t = int64_t(tile0 + i) * kTile + tid;
+      const Weights::Tile x = ahead;
+      if (i + 1 < tiles_per_cta) w.load(ahead, t + kTile, V);
+      const uint64_t v = w.warp_tile_sum(x, t, &top);
+      if (lane == 0) part[i * (kThreads / 32) + warp] = v;
     }
-    if (tid == 0) cta_sum = mine;
+    if (__syncthreads_or(top >= 0x40000000u)) {  // value by value, the bad ones left out
+      for (int i = 0; i < tiles_per_cta; ++i) {
+        const int64_t t0 = int64_t(tile0 + i) * kTile;
+        uint64_t v = 0;
+        for (int j = 0; j < kPer && t0 < V; ++j)
+          v += w.at(static_cast<int>(t0) + j * kThreads + tid, V, &bad);
+        v = warp_sum(v);
+        if (lane == 0) part[i * (kThreads / 32) + warp] = v;
+      }
+      __syncthreads();
+    }
+    for (int i = tid; i < tiles_per_cta; i += kThreads) {
+      uint64_t v = 0;
+      for (int k = 0; k < kThreads / 32; ++k) v += part[i * (kThreads / 32) + k];
+      tile_sum[i] = v;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      uint64_t v = 0;
+      for (int i = lane; i < tiles_per_cta; i += 32) v += tile_sum[i];
+      v = warp_sum(v);
+      if (lane == 0) cta_sum = v;
+    }
     cluster_sync_all();
     uint64_t before = 0, total = 0;
     for (int r = 0; r < cluster; ++r) {
@@ -152,7 +233,7 @@ __global__ void __launch_bounds__(kThreads)
       if (r < rank) before += v;
       total += v;
     }
-    mine = cta_sum;
+    const uint64_t mine = cta_sum;
     cluster_sync_all();  // every CTA has read the sums: they may change, or the CTA leave
     if (total == 0) {    // the same in every CTA of the cluster
       if (w.plain || (!w.q && w.hot < 0)) break;
@@ -227,10 +308,13 @@ extern "C" ts_status ts_verify_drafts(const int32_t* drafts, const int32_t* n_dr
   if (target_stride < V || (draft && draft_stride < V)) return TS_ERR_INVALID_ARG;
   if (V >= kMaxV || n > 65535 || int64_t(B) * kMaxCluster > 2147483647) return TS_ERR_UNSUPPORTED;
   const int tiles = (V + kTile - 1) / kTile;
+  // As many CTAs a request as the GPU holds at once for all of them (two an
+  // SM): a second wave would wait for the first's whole chain of loads.
   int cluster = 1;
-  while (cluster < kMaxCluster && cluster < tiles) cluster *= 2;
+  while (cluster < kMaxCluster && cluster < tiles && int64_t(B) * cluster <= sm_count())
+    cluster *= 2;
   const int per = (tiles + cluster - 1) / cluster;
-  const int smem = per * 8;
+  const int smem = per * 8 * (1 + kThreads / 32);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(B) * cluster);
   cfg.blockDim = dim3(kThreads);

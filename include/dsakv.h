@@ -689,7 +689,7 @@ ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_t* cu_q, in
  *   accepted int32 [B]           out: a
  * A row's probabilities lie in [0, 2) and add up to less than 16; one that is
  * NaN, negative or 2 or more counts as 0 and sets TS_DEVERR_PROB, and so does
- * a row without weight (its next token is -1). n >= 0, V < 2^26; B = 0
+ * a row without weight (its next token is -1). n >= 0, V < 2^23; B = 0
  * enqueues nothing.
  * ------------------------------------------------------------------------- */
 ts_status ts_verify_drafts(const int32_t* drafts, const int32_t* n_draft, const float* target,
