@@ -142,15 +142,21 @@ __device__ __forceinline__ Request request(const Args& a, int b) {
   return r;
 }
 __device__ __forceinline__ int row_tiles(const Args& a, const Request& r) {
-  return static_cast<int>((int64_t(r.n) * a.H + kRows - 1) / kRows);
+  return (r.n * a.H + kRows - 1) / kRows;  // (T H < 2^31 - 128)
 }
 // Keys that the last row of row tile j attends to.
 __device__ __forceinline__ int key_end(const Args& a, const Request& r, int j) {
   if (!a.causal) return r.ctx;
-  const int64_t last = min(int64_t(r.n) * a.H - 1, int64_t(j) * kRows + kRows - 1);
-  return max(0, r.ctx - r.n + static_cast<int>(last / a.H) + 1);
+  // (T H < 2^31)
+  const int last = min(r.n * a.H - 1, j * kRows + kRows - 1);
+  return max(0, r.ctx - r.n + last / a.H + 1);
 }
 __device__ __forceinline__ int key_tiles(int end) { return max(1, (end + kKeys - 1) / kKeys); }
+// x / y of whole numbers >= 0, in 32 bits where they fit (64-bit division is
+// some 100 clocks of serial code).
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+  return ((x | y) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
+}
 // Units (key tiles) of a request's first j row tiles, in closed form: row tile
 // i before the last ends with token (128 i + 127) / H, so it has
 //   1 + max(0, floor((ctx - n + (128 i + 127) / H) / 256))
@@ -159,14 +165,17 @@ __device__ __forceinline__ int key_tiles(int end) { return max(1, (end + kKeys -
 __device__ __forceinline__ int64_t units_before(const Args& a, const Request& r, int tiles,
                                                 int j) {
   if (!a.causal) return int64_t(j) * key_tiles(r.ctx);
-  const int64_t G = 2 * int64_t(a.H), c = (int64_t(r.ctx - r.n) * a.H + kRows - 1) >> 7;
-  auto below = [&](int64_t N) -> int64_t {  // sum of floor(i / G) over 0 <= i < N
-    if (N <= 0) return 0;
-    const int64_t k = N / G;
-    return G * (k * (k - 1) / 2) + k * (N - k * G);
-  };
+  int64_t s = 0;
   const int m = min(j, tiles - 1);
-  int64_t s = m + below(m + c) - below(c);
+  if (m > 0) {
+    const int64_t G = 2 * int64_t(a.H), c = (int64_t(r.ctx - r.n) * a.H + kRows - 1) >> 7;
+    auto below = [&](int64_t N) -> int64_t {  // sum of floor(i / G) over 0 <= i < N
+      if (N <= 0) return 0;
+      const int64_t k = divide(N, G);
+      return G * (k * (k - 1) / 2) + k * (N - k * G);
+    };
+    s = m + below(m + c) - below(c);
+  }
   if (j == tiles) s += key_tiles(key_end(a, r, tiles - 1));
   return s;
 }
@@ -174,43 +183,47 @@ __device__ __forceinline__ int64_t units_before(const Args& a, const Request& r,
 // The pair's stretch of the line of all units: thread-per-request sums, then
 // the request, row tile and key tile that the stretch begins in.
 __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   auto units_of = [&](int b) -> int64_t {
+    if (b >= a.B) return 0;
     const Request r = request(a, b);
     return r.n ? units_before(a, r, row_tiles(a, r), row_tiles(a, r)) : 0;
   };
-  auto warp_scan = [&](int64_t v) {
+  // inclusive scan over the block; *all gets the sum
+  auto scan = [&](int64_t v, int64_t* all) -> int64_t {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
       if (lane >= d) v += o;
     }
+    if (lane == 31) bars->sum[warp] = v;
+    __syncthreads();
+    *all = 0;
+    for (int w = 0; w < threads >> 5; ++w) {
+      if (w < warp) v += bars->sum[w];
+      *all += bars->sum[w];
+    }
+    __syncthreads();
     return v;
   };
-  int64_t mine = 0;
-  for (int b = tid; b < a.B; b += int(blockDim.x)) mine += units_of(b);
-  mine = warp_scan(mine);
-  if (lane == 31) bars->sum[warp] = mine;
-  __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < (int(blockDim.x) >> 5); ++w) total += bars->sum[w];
-  __syncthreads();
+  // (one request a thread: its sum and its place in the scan are the same)
+  const bool small = a.B <= threads;
+  int64_t mine = units_of(tid), total;
+  for (int b = tid + threads; b < a.B; b += threads) mine += units_of(b);
+  int64_t inc = scan(mine, &total);
   const int64_t pairs = min(int64_t(a.pairs), total);
   const int64_t from = pair < pairs ? total * pair / pairs : 0;
   const int64_t count = pair < pairs ? total * (pair + 1) / pairs - from : 0;
   if (tid == 0) bars->count = count;
   int64_t base = 0;
-  for (int b0 = 0; b0 < a.B && base <= from && count; b0 += int(blockDim.x)) {
+  for (int b0 = 0; b0 < a.B && base <= from && count; b0 += threads) {
     const int b = b0 + tid;
-    const int64_t u = b < a.B ? units_of(b) : 0;
-    const int64_t inc = warp_scan(u);
-    if (lane == 31) bars->sum[warp] = inc;
-    __syncthreads();
-    int64_t before = base + inc - u, all = 0;
-    for (int w = 0; w < (int(blockDim.x) >> 5); ++w) {
-      if (w < warp) before += bars->sum[w];
-      all += bars->sum[w];
+    int64_t u = mine, all = total;
+    if (!small) {
+      u = units_of(b);
+      inc = scan(u, &all);
     }
+    const int64_t before = base + inc - u;
     if (u && from >= before && from < before + u) {
       const Request r = request(a, b);
       const int tiles = row_tiles(a, r);
@@ -225,7 +238,6 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
       bars->start_u = static_cast<int>(from - before - units_before(a, r, tiles, lo));
     }
     base += all;
-    __syncthreads();
   }
   __syncthreads();
 }
@@ -511,10 +523,6 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
   bool ok = true;
   while (ok && walk.next(a, sg)) {
     int here = -1, now = ld.slots_of(sg, sg.t0), next = ld.slots_of(sg, sg.t0 + 1);
-    if (w == 0) {
-      ld.prefetch(now, DSA_ROW_BYTES);
-      ld.prefetch(next, DSA_ROW_BYTES);
-    }
     if (w == 0 || !a.q_dense) {
       if (qn > 0) ok = ld.wait(&ld.bars->q_empty, (qn - 1) & 1);
       if (!ok) break;
@@ -529,6 +537,10 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
       }
     }
     ++qn;
+    if (w == 0) {
+      ld.prefetch(now, DSA_ROW_BYTES);
+      ld.prefetch(next, DSA_ROW_BYTES);
+    }
     for (int t = sg.t0; t <= sg.t1 && ok; ++t) {
       const bool scores = t < sg.t1;
       const int ahead = ld.slots_of(sg, t + 2);
@@ -781,6 +793,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
   const uint64_t wait_ns = a.wait_ns;
 
   launch_dependents();
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(Lay::k8 ? &maps.code : &maps.v);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->full[s], Lay::k8 ? 4 : 2);
@@ -931,54 +948,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
       tc_fence_after();
       const int64_t grow = int64_t(sg.r.q0) * a.H + sg.row0 + rr;  // output row
       const bool valid = rr < sg.rows;
-      if (sg.starts && sg.ends) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        uint4* dst = reinterpret_cast<uint4*>(a.out + grow * DSA_DV + half * 256);
-        uint32_t v[32];
+      // Through shared memory (P's, which is free now), 512 bytes of every row
+      // a pass, so that the stores are whole lines: a thread holds one row's
+      // columns, and stores of 16 bytes at 32 rows each took 5 us a row tile.
+      // Of a row's four segments of 128 dims a thread has one (or, one thread
+      // a lane, two).
+      const bool direct = sg.starts && sg.ends;
+      const int slot = pair * 2 + (sg.starts ? 1 : 0);
+      const int seg_bytes = direct ? 256 : 512;
+      uint8_t* dst = direct ? reinterpret_cast<uint8_t*>(a.out) + (grow - r) * (DSA_DV * 2)
+                            : reinterpret_cast<uint8_t*>(a.opart) +
+                                  (int64_t(slot) * a.part_rows + rr - r) * (DSA_DV * 4);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int mine = min(kRowsCta, sg.rows - int(rank) * kRowsCta);  // rows to store
 #pragma unroll 1
-        for (int c = part * (256 / kParts); c < (part + 1) * (256 / kParts); c += 32) {
-          tmem_ld32(trow + kOCol + c, v);
-          tmem_wait_ld();
-          natural_order<kFmt>(v);
-          if (valid) {
-            uint32_t o[16];
+      for (int pass = 0; pass < (direct ? 2 : 4); ++pass) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float x0 = l > 0.f ? __uint_as_float(v[2 * i]) * inv : 0.f;
-              const float x1 = l > 0.f ? __uint_as_float(v[2 * i + 1]) * inv : 0.f;
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(x0, x1);
-              o[i] = *reinterpret_cast<const uint32_t*>(&h2);
+        for (int k = 0; k < 2 / kParts; ++k) {
+          const int seg = half * 2 + part + k;
+          const uint32_t col = trow + kOCol + (part + k) * 128;
+          uint8_t* stage = p_tile + r * 512 + seg * 128;
+          auto put = [&](int piece, const uint4& x) {
+            *reinterpret_cast<uint4*>(stage + ((piece ^ (r & 7)) << 4)) = x;
+          };
+          uint32_t v[32];
+          if (direct) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              tmem_ld32(col + pass * 64 + h * 32, v);
+              tmem_wait_ld();
+              natural_order<kFmt>(v);
+              uint32_t o[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                // (a row without a key has no O: zeros, whatever lies there)
+                const float x0 = l > 0.f ? __uint_as_float(v[2 * i]) * inv : 0.f;
+                const float x1 = l > 0.f ? __uint_as_float(v[2 * i + 1]) * inv : 0.f;
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(x0, x1);
+                o[i] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                put(h * 4 + j, make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              dst[c / 8 + j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          }
-        }
-        if (valid && half == 0 && part == 0 && a.lse)
-          a.lse[grow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-      } else {
-        const int slot = pair * 2 + (sg.starts ? 1 : 0);
-        const int64_t prow = int64_t(slot) * a.part_rows + rr;
-        float4* dst = reinterpret_cast<float4*>(a.opart + prow * DSA_DV + half * 256);
-        uint32_t v[32];
-#pragma unroll 1
-        for (int c = part * (256 / kParts); c < (part + 1) * (256 / kParts); c += 32) {
-          tmem_ld32(trow + kOCol + c, v);
-          tmem_wait_ld();
-          natural_order<kFmt>(v);
-          if (valid) {
+          } else {
+            tmem_ld32(col + pass * 32, v);
+            tmem_wait_ld();
+            natural_order<kFmt>(v);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              dst[c / 4 + j] =
-                  make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                              __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+              put(j, make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
           }
         }
-        if (valid && half == 0 && part == 0) a.ml[prow] = make_float2(m, l);
-        if (rank == 0 && threadIdx.x == 0)
-          a.meta[slot] = make_int4(static_cast<int>(int64_t(sg.r.q0) * a.H + sg.row0), sg.rows,
-                                   (sg.starts ? kStarts : 0) | (sg.ends ? kEnds : 0), 0);
+        softmax_sync<32 * Lay::kSoftmaxWarps>();
+        for (int i = warp; i < mine; i += kSoftmaxWarps)
+          *reinterpret_cast<uint4*>(dst + int64_t(i) * seg_bytes * 4 + (lane >> 3) * seg_bytes +
+                                    pass * 128 + (lane & 7) * 16) =
+              *reinterpret_cast<const uint4*>(p_tile + i * 512 + (lane >> 3) * 128 +
+                                              (((lane & 7) ^ (i & 7)) << 4));
+        softmax_sync<32 * Lay::kSoftmaxWarps>();
       }
+      if (valid && half == 0 && part == 0) {
+        if (!direct) a.ml[int64_t(slot) * a.part_rows + rr] = make_float2(m, l);
+        else if (a.lse) a.lse[grow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      }
+      if (!direct && rank == 0 && threadIdx.x == 0)
+        a.meta[slot] = make_int4(static_cast<int>(int64_t(sg.r.q0) * a.H + sg.row0), sg.rows,
+                                 (sg.starts ? kStarts : 0) | (sg.ends ? kEnds : 0), 0);
       tc_fence_before();
     }
   } else if (warp < kMmaWarp) {
