@@ -113,7 +113,7 @@ struct Args {
   int64_t table_stride;
   int page_shift;
   const int32_t* ctx_len;
-  int causal;
+  bool causal;
   float scale_log2;  // |scale| log2(e)
   bool negate;       // scale < 0
   __nv_bfloat16* out;
@@ -145,16 +145,16 @@ __device__ __forceinline__ int row_tiles(const Args& a, const Request& r) {
   return (r.n * a.H + kRows - 1) / kRows;  // (T H < 2^31 - 128)
 }
 // Keys that the last row of row tile j attends to.
-__device__ __forceinline__ int key_end(const Args& a, const Request& r, int j) {
-  if (!a.causal) return r.ctx;
+__device__ __forceinline__ int key_end(int H, bool causal, const Request& r, int j) {
+  if (!causal) return r.ctx;
   // (T H < 2^31)
-  const int last = min(r.n * a.H - 1, j * kRows + kRows - 1);
-  return max(0, r.ctx - r.n + last / a.H + 1);
+  const int last = min(r.n * H - 1, j * kRows + kRows - 1);
+  return max(0, r.ctx - r.n + last / H + 1);
 }
 __device__ __forceinline__ int key_tiles(int end) { return max(1, (end + kKeys - 1) / kKeys); }
 // x / y of whole numbers >= 0, in 32 bits where they fit (64-bit division is
 // some 100 clocks of serial code).
-__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+__device__ __noinline__ int64_t divide(int64_t x, int64_t y) {
   return ((x | y) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
 }
 // Units (key tiles) of a request's first j row tiles, in closed form: row tile
@@ -162,13 +162,13 @@ __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
 //   1 + max(0, floor((ctx - n + (128 i + 127) / H) / 256))
 //     = 1 + max(0, floor((i + c) / 2H)),  c = floor(((ctx - n) H + 127) / 128)
 // key tiles (nested floors of quotients fold into one).
-__device__ __forceinline__ int64_t units_before(const Args& a, const Request& r, int tiles,
-                                                int j) {
-  if (!a.causal) return int64_t(j) * key_tiles(r.ctx);
+__device__ __noinline__ int64_t units_before(int H, bool causal, const Request r, int tiles,
+                                             int j) {
+  if (!causal) return int64_t(j) * key_tiles(r.ctx);
   int64_t s = 0;
   const int m = min(j, tiles - 1);
   if (m > 0) {
-    const int64_t G = 2 * int64_t(a.H), c = (int64_t(r.ctx - r.n) * a.H + kRows - 1) >> 7;
+    const int64_t G = 2 * int64_t(H), c = (int64_t(r.ctx - r.n) * H + kRows - 1) >> 7;
     auto below = [&](int64_t N) -> int64_t {  // sum of floor(i / G) over 0 <= i < N
       if (N <= 0) return 0;
       const int64_t k = divide(N, G);
@@ -176,7 +176,7 @@ __device__ __forceinline__ int64_t units_before(const Args& a, const Request& r,
     };
     s = m + below(m + c) - below(c);
   }
-  if (j == tiles) s += key_tiles(key_end(a, r, tiles - 1));
+  if (j == tiles) s += key_tiles(key_end(H, causal, r, tiles - 1));
   return s;
 }
 
@@ -187,7 +187,7 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
   auto units_of = [&](int b) -> int64_t {
     if (b >= a.B) return 0;
     const Request r = request(a, b);
-    return r.n ? units_before(a, r, row_tiles(a, r), row_tiles(a, r)) : 0;
+    return r.n ? units_before(a.H, a.causal, r, row_tiles(a, r), row_tiles(a, r)) : 0;
   };
   // inclusive scan over the block; *all gets the sum
   auto scan = [&](int64_t v, int64_t* all) -> int64_t {
@@ -199,6 +199,7 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
     if (lane == 31) bars->sum[warp] = v;
     __syncthreads();
     *all = 0;
+#pragma unroll 1
     for (int w = 0; w < threads >> 5; ++w) {
       if (w < warp) v += bars->sum[w];
       *all += bars->sum[w];
@@ -208,14 +209,16 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
   };
   // (one request a thread: its sum and its place in the scan are the same)
   const bool small = a.B <= threads;
-  int64_t mine = units_of(tid), total;
-  for (int b = tid + threads; b < a.B; b += threads) mine += units_of(b);
+  int64_t mine = 0, total;
+#pragma unroll 1
+  for (int b = tid; b < a.B; b += threads) mine += units_of(b);
   int64_t inc = scan(mine, &total);
   const int64_t pairs = min(int64_t(a.pairs), total);
-  const int64_t from = pair < pairs ? total * pair / pairs : 0;
-  const int64_t count = pair < pairs ? total * (pair + 1) / pairs - from : 0;
+  const int64_t from = pair < pairs ? divide(total * pair, pairs) : 0;
+  const int64_t count = pair < pairs ? divide(total * (pair + 1), pairs) - from : 0;
   if (tid == 0) bars->count = count;
   int64_t base = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.B && base <= from && count; b0 += threads) {
     const int b = b0 + tid;
     int64_t u = mine, all = total;
@@ -228,14 +231,15 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
       const Request r = request(a, b);
       const int tiles = row_tiles(a, r);
       int lo = 0, hi = tiles - 1;  // the last row tile that begins at or before `from`
+#pragma unroll 1
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (units_before(a, r, tiles, mid) <= from - before) lo = mid;
+        if (units_before(a.H, a.causal, r, tiles, mid) <= from - before) lo = mid;
         else hi = mid - 1;
       }
       bars->start_b = b;
       bars->start_j = lo;
-      bars->start_u = static_cast<int>(from - before - units_before(a, r, tiles, lo));
+      bars->start_u = static_cast<int>(from - before - units_before(a.H, a.causal, r, tiles, lo));
     }
     base += all;
   }
@@ -245,6 +249,7 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
 // Reports lengths out of range (once per launch).
 __device__ __forceinline__ void check_lengths(const Args& a) {
   const int64_t most = min(a.table_stride << a.page_shift, int64_t(1) << 30);
+#pragma unroll 1
   for (int b = threadIdx.x; b < a.B; b += int(blockDim.x)) {
     const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1), ctx = __ldg(a.ctx_len + b);
     if (c0 < 0 || c1 < c0 || c1 > a.T) report(a.err, TS_DEVERR_ORDER);
@@ -279,7 +284,7 @@ struct Walk {
     s.b = b;
     s.row0 = j * kRows;
     s.rows = static_cast<int>(min(int64_t(kRows), int64_t(s.r.n) * a.H - s.row0));
-    s.end = key_end(a, s.r, j);
+    s.end = key_end(a.H, a.causal, s.r, j);
     const int units = key_tiles(s.end);
     s.t0 = u;
     s.t1 = static_cast<int>(min(int64_t(units), u + left));
@@ -451,12 +456,14 @@ struct Loader {
   }
   // ... or, tokens further apart, row by row by `warps` warps.
   __device__ __forceinline__ void q_by_copy(int row0, int rows, int w, int warps) {
+#pragma unroll 1
     for (int i = w; i < kRowsCta; i += warps) {
       const int rr = rank * kRowsCta + i;
       const bool valid = rr < rows;
       const int row = row0 + (valid ? rr : 0);
       const uint8_t* src =
           a.q + int64_t(row / a.H) * a.q_stride + int64_t(row % a.H) * DSA_ROW_BYTES;
+#pragma unroll 1
       for (int c = lane; c < DSA_ROW_CHUNKS; c += 32)
         cp_async16_zfill(q_tile + (c >> 3) * kQBlock + i * 128 + (((c & 7) ^ (i & 7)) << 4),
                          src + c * 16, valid);
@@ -468,6 +475,7 @@ struct Loader {
     const uint32_t boxes = __popc(__ballot_sync(
         0xffffffffu, slots >= 0 && lane >> 3 == int(rank) && (lane & (k_step - 1)) == 0));
     if (el) mbar_expect_tx_cluster(bar, boxes * k_step * 2048);
+#pragma unroll 1
     for (int i = 0; i < 8; i += k_step) {
       const int slot = __shfl_sync(0xffffffffu, slots, rank * 8 + i);
       if (slot >= 0 && el) tma_load_3d_pair(dst + i * 2048, &maps.k, bar, 0, slot, kb);
@@ -480,6 +488,7 @@ struct Loader {
     if (key0 + 64 > ctx || gaps) {
       // V rows that are not the request's must be zeros: their weights are,
       // but the rows may hold anything, and 0 times NaN is NaN
+#pragma unroll 4
       for (int i = 0; i < 32; ++i) {
         const int row = i * 2 + (lane >> 4), c = lane & 15;  // a row's 16 pieces
         int slot = __shfl_sync(0xffffffffu, slots, g * 4 + (row >> 4));
@@ -495,6 +504,7 @@ struct Loader {
       return;
     }
     if (el) mbar_expect_tx_cluster(bar, kStageBytes);
+#pragma unroll 1
     for (int i = 0; i < 4; i += v_step) {
       const int slot = __shfl_sync(0xffffffffu, slots, g * 4 + i);
       if (el) {
@@ -553,6 +563,7 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
         }
       }
       const int n = stages_of(sg, t);
+#pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
         if (turn == w) {
           ok = ld.wait_free(s, wrap);
@@ -702,6 +713,7 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
           if (boxes) mbar_expect_tx(raw_bar, __popc(boxes) * ld.v_step * 1024);
           else mbar_arrive(raw_bar);
         }
+#pragma unroll 1
         for (int k = 0; k < 4; k += ld.v_step) {
           const int slot = __shfl_sync(0xffffffffu, slots, k);
           if (slot >= 0 && ld.el)
@@ -722,6 +734,7 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
       if (first) {  // Q's latent part into the codes' order
         if (!ld.wait(&bars->q_raw, qn & 1)) break;
         ++qn;
+#pragma unroll 2
         for (int k = w * 32 + lane; k < kRowsCta * 64; k += kConvertWarps * 32) {
           uint4* x = reinterpret_cast<uint4*>(ld.q_tile) + k;
           *x = code_order(*x);
@@ -735,6 +748,7 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
       if (rope) {  // bf16 as it is, by TMA
         const uint32_t boxes = valid & (ld.v_step == 4 ? 1u : ld.v_step == 2 ? 5u : 15u);
         if (ld.el) mbar_expect_tx_cluster(bar, __popc(boxes) * ld.v_step * 2048);
+#pragma unroll 1
         for (int k = 0; k < 4; k += ld.v_step) {
           const int slot = __shfl_sync(0xffffffffu, unit_slots, k);
           if (slot >= 0 && ld.el) tma_load_3d_pair(dst + k * 2048, &ld.maps.k, bar, 0, slot, 0);
@@ -1001,6 +1015,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
           }
         }
         softmax_sync<32 * Lay::kSoftmaxWarps>();
+#pragma unroll 2
         for (int i = warp; i < mine; i += kSoftmaxWarps)
           *reinterpret_cast<uint4*>(dst + int64_t(i) * seg_bytes * 4 + (lane >> 3) * seg_bytes +
                                     pass * 128 + (lane & 7) * 16) =
@@ -1074,7 +1089,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
         for (int t = sg.t0; t <= sg.t1 && ok; ++t) {
           if (t < sg.t1) {
             const uint32_t d = tmem + (tg & 1) * 128;
-#pragma unroll
+#pragma unroll 1
             for (int kb = 0; kb < kBlocks; kb += 3) {
               if (!landed(3)) break;
 #pragma unroll
@@ -1105,6 +1120,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
             tc_fence_after();
             const int g1 = groups(sg.end, t - 1);
             const bool first = t - 1 == sg.t0;
+#pragma unroll 1
             for (int g = 0; g < g1 && landed(2); ++g) {
               const uint64_t pd = p_desc + g * (kPBlock >> 4);
 #pragma unroll
@@ -1175,37 +1191,25 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Arg
   auto row_of = [&](int i) -> int64_t {
     return int64_t(i == 0 ? pair * 2 + 1 : (pair + i) * 2) * a.part_rows + r;
   };
-  constexpr int kPer = (kMaxPairs + 31) / 32;
-  float w[kPer], l[kPer], mx = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int i = lane + 32 * k;
-    const float2 e = i < parts ? a.ml[row_of(i)] : make_float2(-INFINITY, 0.f);
-    w[k] = e.x;
-    l[k] = e.y;
-    mx = fmaxf(mx, e.x);
-  }
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, a.ml[row_of(i)].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-  float sum = 0.f;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    w[k] = mx == -INFINITY ? 0.f : exp2f(w[k] - mx);
-    sum += w[k] * l[k];
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  float acc[16];
+  const float base = mx == -INFINITY ? 0.f : mx;
+  float sum = 0.f, acc[16];
 #pragma unroll
   for (int c = 0; c < 16; ++c) acc[c] = 0.f;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int n = min(parts - 32 * k, 32);
+#pragma unroll 1
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const float2 e = i0 + lane < parts ? a.ml[row_of(i0 + lane)] : make_float2(-INFINITY, 0.f);
+    const float w = exp2f(e.x - base);
+    sum += w * e.y;
+    const int n = min(parts - i0, 32);
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w[k], i);
-      const float4* src =
-          reinterpret_cast<const float4*>(a.opart + row_of(32 * k + i) * DSA_DV) + lane;
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float4* src = reinterpret_cast<const float4*>(a.opart + row_of(i0 + i) * DSA_DV) + lane;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float4 x = __ldcs(src + 32 * c);
@@ -1216,6 +1220,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Arg
       }
     }
   }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   const int64_t row = int64_t(head.x) + r;
   uint2* dst = reinterpret_cast<uint2*>(a.out + row * DSA_DV) + lane;
@@ -1306,7 +1312,7 @@ extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_
   a.table_stride = table_stride;
   a.page_shift = __builtin_ctz(page_size);
   a.ctx_len = ctx_len;
-  a.causal = causal;
+  a.causal = causal != 0;
   // (above 0: a masked score, minus infinity, times 0 would be no number)
   a.scale_log2 = std::max(std::fabs(scale) * kLog2e, FLT_MIN);
   a.negate = scale < 0.f;

@@ -511,25 +511,32 @@ __device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t* bar, uint32_t p
 // and four products took 518 clocks on GB300, converged 257 (the products'
 // own time).
 template <bool kCluster>
+__device__ __forceinline__ bool mbar_warp_test(uint64_t* bar, uint32_t parity, bool poll) {
+  bool ok;
+  if (kCluster) ok = poll ? mbar_test_wait_cluster(bar, parity) : mbar_try_wait_cluster(bar, parity);
+  else ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+// (The time in 32 bits, and so a limit of 4 s at most: a kernel has some twenty
+// such waits, and its code has to fit the instruction caches.)
+template <bool kCluster>
 __device__ __forceinline__ bool mbar_warp_wait(uint64_t* bar, uint32_t parity,
                                                volatile int* abort, uint64_t limit_ns) {
-  const bool short_limit = limit_ns < kShortWaitNs;
-  auto test = [&]() -> bool {
-    bool ok;
-    if (kCluster)
-      ok = short_limit ? mbar_test_wait_cluster(bar, parity) : mbar_try_wait_cluster(bar, parity);
-    else
-      ok = short_limit ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
-    return __all_sync(0xffffffffu, ok) != 0;
+  if (mbar_warp_test<kCluster>(bar, parity, true)) return true;
+  auto now = []() -> uint32_t {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
   };
-  if (test()) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
-    if (test()) return true;
-    const bool late = globaltimer_ns() - t0 > limit_ns;
+  const uint32_t limit = static_cast<uint32_t>(limit_ns < 4000000000ull ? limit_ns : 4000000000ull);
+  const bool poll = limit < kShortWaitNs;
+  const uint32_t t0 = now();
+  while (!mbar_warp_test<kCluster>(bar, parity, poll)) {
+    const bool late = now() - t0 > limit;
     if (late) *abort = 1;
     if (__any_sync(0xffffffffu, late || *abort != 0)) return false;
   }
+  return true;
 }
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
