@@ -69,6 +69,7 @@ struct Layout {
 };
 constexpr int kMaxStages = 7;
 constexpr int kMaxPairs = 80;
+constexpr int kMaxCtx = 1 << 27;  // with H <= 1024, every count of the plan fits 32 bits
 constexpr uint32_t kOCol = 256;  // TMEM columns: S buffers 0..127 and 128..255, O 256..511
 constexpr uint64_t kWaitLimit = 2000000000ull;  // 2 s of global timer per wait
 constexpr uint64_t kDrainNs = 2000000ull;
@@ -112,6 +113,7 @@ struct Args {
   const int32_t* block_table;
   int64_t table_stride;
   int page_shift;
+  int max_ctx;  // positions that the table has room for, at most kMaxCtx
   const int32_t* ctx_len;
   bool causal;
   float scale_log2;  // |scale| log2(e)
@@ -137,8 +139,7 @@ __device__ __forceinline__ Request request(const Args& a, int b) {
   Request r;
   r.q0 = min(max(__ldg(a.cu_q + b), 0), a.T);
   r.n = max(min(__ldg(a.cu_q + b + 1), a.T) - r.q0, 0);
-  const int64_t most = min(a.table_stride << a.page_shift, int64_t(1) << 30);
-  r.ctx = static_cast<int>(min(int64_t(max(__ldg(a.ctx_len + b), 0)), most));
+  r.ctx = min(max(__ldg(a.ctx_len + b), 0), a.max_ctx);
   return r;
 }
 __device__ __forceinline__ int row_tiles(const Args& a, const Request& r) {
@@ -154,8 +155,8 @@ __device__ __forceinline__ int key_end(int H, bool causal, const Request& r, int
 __device__ __forceinline__ int key_tiles(int end) { return max(1, (end + kKeys - 1) / kKeys); }
 // x / y of whole numbers >= 0, in 32 bits where they fit (64-bit division is
 // some 100 clocks of serial code).
-__device__ __noinline__ int64_t divide(int64_t x, int64_t y) {
-  return ((x | y) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
+__device__ __noinline__ int64_t divide(int64_t x, int y) {
+  return (x >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
 }
 // Units (key tiles) of a request's first j row tiles, in closed form: row tile
 // i before the last ends with token (128 i + 127) / H, so it has
@@ -168,11 +169,11 @@ __device__ __noinline__ int64_t units_before(int H, bool causal, const Request r
   int64_t s = 0;
   const int m = min(j, tiles - 1);
   if (m > 0) {
-    const int64_t G = 2 * int64_t(H), c = (int64_t(r.ctx - r.n) * H + kRows - 1) >> 7;
-    auto below = [&](int64_t N) -> int64_t {  // sum of floor(i / G) over 0 <= i < N
-      if (N <= 0) return 0;
-      const int64_t k = divide(N, G);
-      return G * (k * (k - 1) / 2) + k * (N - k * G);
+    const uint32_t G = 2 * H;
+    const int c = static_cast<int>((int64_t(r.ctx - r.n) * H + kRows - 1) >> 7);
+    auto below = [&](int N) -> int64_t {  // sum of floor(i / G) over 0 <= i < N
+      const uint32_t x = max(N, 0), k = x / G;
+      return int64_t(G) * (int64_t(k) * (k - 1) / 2) + int64_t(k) * (x - k * G);
     };
     s = m + below(m + c) - below(c);
   }
@@ -213,9 +214,11 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
 #pragma unroll 1
   for (int b = tid; b < a.B; b += threads) mine += units_of(b);
   int64_t inc = scan(mine, &total);
-  const int64_t pairs = min(int64_t(a.pairs), total);
-  const int64_t from = pair < pairs ? divide(total * pair, pairs) : 0;
-  const int64_t count = pair < pairs ? divide(total * (pair + 1), pairs) - from : 0;
+  const int pairs = static_cast<int>(min(int64_t(a.pairs), total));
+  const int64_t share = pairs ? divide(total, pairs) : 0;
+  const int more = static_cast<int>(total - share * pairs);  // pairs with one unit more
+  const int64_t from = share * pair + min(pair, more);
+  const int64_t count = pair < pairs ? share + (pair < more ? 1 : 0) : 0;
   if (tid == 0) bars->count = count;
   int64_t base = 0;
 #pragma unroll 1
@@ -248,12 +251,11 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
 
 // Reports lengths out of range (once per launch).
 __device__ __forceinline__ void check_lengths(const Args& a) {
-  const int64_t most = min(a.table_stride << a.page_shift, int64_t(1) << 30);
 #pragma unroll 1
   for (int b = threadIdx.x; b < a.B; b += int(blockDim.x)) {
     const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1), ctx = __ldg(a.ctx_len + b);
     if (c0 < 0 || c1 < c0 || c1 > a.T) report(a.err, TS_DEVERR_ORDER);
-    if (ctx < 0 || ctx > most) report(a.err, TS_DEVERR_CTX);
+    if (ctx < 0 || ctx > a.max_ctx) report(a.err, TS_DEVERR_CTX);
   }
 }
 
@@ -470,16 +472,31 @@ struct Loader {
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
-  // K stage: this CTA's 128 keys of a tile, 64 dims of block kb.
-  __device__ __forceinline__ void k_by_tma(int slots, int kb, uint8_t* dst, uint32_t bar) {
-    const uint32_t boxes = __popc(__ballot_sync(
-        0xffffffffu, slots >= 0 && lane >> 3 == int(rank) && (lane & (k_step - 1)) == 0));
-    if (el) mbar_expect_tx_cluster(bar, boxes * k_step * 2048);
-#pragma unroll 1
-    for (int i = 0; i < 8; i += k_step) {
-      const int slot = __shfl_sync(0xffffffffu, slots, rank * 8 + i);
-      if (slot >= 0 && el) tma_load_3d_pair(dst + i * 2048, &maps.k, bar, 0, slot, kb);
+  // K stage: this CTA's 128 keys of a tile, 64 dims of block kb; box i of the
+  // tile starts at slot[i]. (Unrolled: a TMA costs its warp 50 clocks so, and
+  // 97 in a loop that shuffles its slot first.)
+  struct KBoxes {
+    int slot[8];
+    uint32_t bytes;
+  };
+  __device__ __forceinline__ KBoxes k_boxes(int slots) {
+    KBoxes k;
+    uint32_t boxes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      k.slot[i] = __shfl_sync(0xffffffffu, slots, rank * 8 + i);
+      if (i & (k_step - 1)) k.slot[i] = -1;
+      boxes += k.slot[i] >= 0;
     }
+    k.bytes = boxes * k_step * 2048;
+    return k;
+  }
+  __device__ __forceinline__ void k_by_tma(const KBoxes& k, int kb, uint8_t* dst, uint32_t bar) {
+    if (!el) return;
+    mbar_expect_tx_cluster(bar, k.bytes);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k.slot[i] >= 0) tma_load_3d_pair(dst + i * 2048, &maps.k, bar, 0, k.slot[i], kb);
   }
   // V stage: 64 keys from key0 on (group g of the tile), dims of blocks kb, kb + 1.
   __device__ __forceinline__ void v_by_tma(int slots, int key0, int ctx, int g, int kb,
@@ -503,14 +520,16 @@ struct Loader {
       if (el) mbar_arrive_cluster(bar);
       return;
     }
-    if (el) mbar_expect_tx_cluster(bar, kStageBytes);
-#pragma unroll 1
-    for (int i = 0; i < 4; i += v_step) {
-      const int slot = __shfl_sync(0xffffffffu, slots, g * 4 + i);
-      if (el) {
-        tma_load_3d_pair(dst + i * 2048, &maps.v, bar, 0, slot, kb);
-        if (v_step < 4) tma_load_3d_pair(dst + kVBox + i * 2048, &maps.v, bar, 0, slot, kb + 1);
-      }
+    int slot[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) slot[i] = __shfl_sync(0xffffffffu, slots, g * 4 + i);
+    if (!el) return;
+    mbar_expect_tx_cluster(bar, kStageBytes);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & (v_step - 1)) continue;
+      tma_load_3d_pair(dst + i * 2048, &maps.v, bar, 0, slot[i], kb);
+      if (v_step < 4) tma_load_3d_pair(dst + kVBox + i * 2048, &maps.v, bar, 0, slot[i], kb + 1);
     }
   }
 };
@@ -563,6 +582,7 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
         }
       }
       const int n = stages_of(sg, t);
+      const Loader::KBoxes k = ld.k_boxes(now);
 #pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
         if (turn == w) {
@@ -571,7 +591,7 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
             uint8_t* dst = ld.ring + s * kStageBytes;
             const uint32_t bar = ld.full + s * 8;
             if (scores && i < kBlocks) {
-              ld.k_by_tma(now, i, dst, bar);
+              ld.k_by_tma(k, i, dst, bar);
             } else {
               const int v = scores ? i - kBlocks : i;
               ld.v_by_tma(here, (t - 1) * kKeys + (v >> 1) * 64, sg.r.ctx, v >> 1,
@@ -709,15 +729,16 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
       slots = __shfl_sync(0xffffffffu, slots, (step + lane) & 31);
       if (!next_rope) {
         const uint32_t boxes = next_valid & (ld.v_step == 4 ? 1u : ld.v_step == 2 ? 5u : 15u);
+        int at[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) at[k] = __shfl_sync(0xffffffffu, slots, k);
         if (ld.el) {
           if (boxes) mbar_expect_tx(raw_bar, __popc(boxes) * ld.v_step * 1024);
           else mbar_arrive(raw_bar);
-        }
-#pragma unroll 1
-        for (int k = 0; k < 4; k += ld.v_step) {
-          const int slot = __shfl_sync(0xffffffffu, slots, k);
-          if (slot >= 0 && ld.el)
-            tma_load_3d(raw + k * 1024, &ld.maps.code, raw_bar, kb * 64, slot, 0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (boxes >> k & 1)
+              tma_load_3d(raw + k * 1024, &ld.maps.code, raw_bar, kb * 64, at[k], 0);
         }
         // (without a condition, which would wait for the values here)
         const int slot0 = max(__shfl_sync(0xffffffffu, slots, lane >> 4), 0) + (lane & 15);
@@ -1311,6 +1332,8 @@ extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_
   a.block_table = block_table;
   a.table_stride = table_stride;
   a.page_shift = __builtin_ctz(page_size);
+  a.max_ctx = static_cast<int>(
+      std::min(std::min(table_stride, int64_t(kMaxCtx)) * page_size, int64_t(kMaxCtx)));
   a.ctx_len = ctx_len;
   a.causal = causal != 0;
   // (above 0: a masked score, minus infinity, times 0 would be no number)

@@ -73,7 +73,9 @@ def test_stretches_cover_every_unit_once(pairs):
         total, got, cut = len(line), [], []
         P = min(pairs, total)
         for p in range(P):
-            lo, hi = total * p // P, total * (p + 1) // P
+            share, more = divmod(total, P)
+            lo = share * p + min(p, more)
+            hi = lo + share + (p < more)
             assert hi > lo
             segments = {}
             for b, j, t in line[lo:hi]:
