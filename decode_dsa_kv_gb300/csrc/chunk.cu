@@ -1080,24 +1080,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
       const bool el = elect_one();
       uint32_t s = 0, phase = 0, tg = 0, qn = 0;
       bool ok = true;
-      // the next `count` stages, in both CTAs (the waits of several stages
-      // overlap: a stage's own wait, vote and election cost 220-350 clocks of
-      // this warp, more than the 257 of its four products if taken one by one)
-      auto landed = [&](const int count) -> bool {
-        bool all = true;
-        uint32_t s1 = s, phase1 = phase;
-#pragma unroll
-        for (int i = 0; i < count; ++i) {
-          all &= mbar_try_wait(&bars->full[s1], phase1);
-          if (++s1 == kStages) s1 = 0, phase1 ^= 1;
-        }
-        if (!__all_sync(0xffffffffu, all)) {
-          s1 = s, phase1 = phase;
-          for (int i = 0; i < count && ok; ++i) {
-            ok = mbar_warp_wait<false>(&bars->full[s1], phase1, abort, wait_ns);
-            if (++s1 == kStages) s1 = 0, phase1 ^= 1;
-          }
-        }
+      // the next stage, in both CTAs
+      auto landed = [&]() -> bool {
+        if (!__all_sync(0xffffffffu, mbar_try_wait(&bars->full[s], phase)))
+          ok = mbar_warp_wait<false>(&bars->full[s], phase, abort, wait_ns);
         tc_fence_after();
         return ok;
       };
@@ -1111,20 +1097,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
           if (t < sg.t1) {
             const uint32_t d = tmem + (tg & 1) * 128;
 #pragma unroll 1
-            for (int kb = 0; kb < kBlocks; kb += 3) {
-              if (!landed(3)) break;
+            for (int kb = 0; kb < kBlocks && landed(); ++kb) {
+              const uint64_t qd = q_desc + kb * (kQBlock >> 4);
+              const uint64_t kd = k_desc + s * (kStageBytes >> 4);
+              if (el) {
 #pragma unroll
-              for (int i = 0; i < 3; ++i) {
-                const uint64_t qd = q_desc + (kb + i) * (kQBlock >> 4);
-                const uint64_t kd = k_desc + s * (kStageBytes >> 4);
-                if (el) {
-#pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_bf16_pair(d, qd + kk * 2, kd + kk * 2, id_s, (kb | i | kk) != 0);
-                  tc_commit_pair(&bars->empty[phase][s]);
-                }
-                advance();
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma_bf16_pair(d, qd + kk * 2, kd + kk * 2, id_s, (kb | kk) != 0);
+                tc_commit_pair(&bars->empty[phase][s]);
               }
+              advance();
             }
             if (!ok) break;
             if (el) {
@@ -1142,20 +1124,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
             const int g1 = groups(sg.end, t - 1);
             const bool first = t - 1 == sg.t0;
 #pragma unroll 1
-            for (int g = 0; g < g1 && landed(2); ++g) {
-              const uint64_t pd = p_desc + g * (kPBlock >> 4);
+            for (int v = 0; v < 2 * g1 && landed(); ++v) {  // group v / 2, dims half v % 2
+              const uint64_t pd = p_desc + (v >> 1) * (kPBlock >> 4);
+              const uint64_t vd = v_desc + s * (kStageBytes >> 4);
+              const uint32_t d = tmem + kOCol + (v & 1) * 128;
+              if (el) {
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint64_t vd = v_desc + s * (kStageBytes >> 4);
-                if (el) {
-#pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_bf16_pair(tmem + kOCol + j * 128, pd + kk * 2, vd + kk * (2048 >> 4),
-                                     id_pv, !first || (g | kk) != 0);
-                  tc_commit_pair(&bars->empty[phase][s]);
-                }
-                advance();
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma_bf16_pair(d, pd + kk * 2, vd + kk * (2048 >> 4), id_pv,
+                                   !first || (v >> 1 | kk) != 0);
+                tc_commit_pair(&bars->empty[phase][s]);
               }
+              advance();
             }
             if (ok && el) tc_commit_pair(&bars->pv_done);
           }
