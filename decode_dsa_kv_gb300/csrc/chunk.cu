@@ -419,16 +419,23 @@ struct Loader {
   __device__ __forceinline__ bool wait_free(uint32_t s, uint32_t wrap) {
     return wrap == 0 || wait(&bars->empty[(wrap - 1) & 1][s], ((wrap - 1) >> 1) & 1);
   }
-  // The slot of every 16-key step of a segment's key tile: lanes 0..15 (-1:
-  // no such page; keys past the context need none).
-  __device__ __forceinline__ int slots_of(const Segment& g, int t) {
-    const int key = t * kKeys + lane * 16;
-    if (lane >= 16 || key >= g.r.ctx || t >= g.t1) return -1;
-    const int64_t page = __ldg(a.block_table + g.b * a.table_stride + (key >> a.page_shift));
+  // The slot of every 16-key step of a segment's key tile t: lanes 0..15 (-1:
+  // no such page; keys past the context need none). In two halves: the loaders
+  // of bf16 rows read the table's entries a tile before they use them.
+  __device__ __forceinline__ bool needs(const Segment& g, int t) {
+    return lane < 16 && t < g.t1 && t * kKeys + lane * 16 < g.r.ctx;
+  }
+  __device__ __forceinline__ int pages_of(const Segment& g, int t) {
+    if (!needs(g, t)) return -1;
+    return __ldg(a.block_table + g.b * a.table_stride + ((t * kKeys + lane * 16) >> a.page_shift));
+  }
+  __device__ __forceinline__ int slots_of(const Segment& g, int t, int64_t page) {
+    if (!needs(g, t)) return -1;
     if (page < 0 || page >= a.pages) {
       report(a.err, TS_DEVERR_SLOT_RANGE);
       return -1;
     }
+    const int key = t * kKeys + lane * 16;
     return static_cast<int>((page << a.page_shift) + (key & ((1 << a.page_shift) - 1)));
   }
   // Q of a row tile that starts at output row `row0`: by TMA (rows past the
@@ -542,7 +549,7 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
   int turn = 0;  // whose stage is next
   bool ok = true;
   while (ok && walk.next(a, sg)) {
-    int here = -1, now = ld.slots_of(sg, sg.t0), next = ld.slots_of(sg, sg.t0 + 1);
+    int here = -1, now_page = ld.pages_of(sg, sg.t0), next_page = ld.pages_of(sg, sg.t0 + 1);
     if (w == 0 || !a.q_dense) {
       if (qn > 0) ok = ld.wait(&ld.bars->q_empty, (qn - 1) & 1);
       if (!ok) break;
@@ -559,7 +566,9 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
     ++qn;
     for (int t = sg.t0; t <= sg.t1 && ok; ++t) {
       const bool scores = t < sg.t1;
-      const int ahead = ld.slots_of(sg, t + 2);
+      const int now = ld.slots_of(sg, t, now_page);
+      now_page = next_page;
+      next_page = ld.pages_of(sg, t + 2);
       const int n = stages_of(sg, t);
       const Loader::KBoxes k = ld.k_boxes(now);
 #pragma unroll 1
@@ -582,8 +591,6 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
         if (++s == kStages) s = 0, ++wrap;
       }
       here = now;
-      now = next;
-      next = ahead;
     }
   }
 }
@@ -651,10 +658,10 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
         inside = fresh = true;
         t = sg.t0;
         here = -1;
-        now = ld.slots_of(sg, t);
+        now = ld.slots_of(sg, t, ld.pages_of(sg, t));
       }
       n = 2 * stages_of(sg, t);
-      next = ld.slots_of(sg, t + 1);
+      next = ld.slots_of(sg, t + 1, ld.pages_of(sg, t + 1));
     }
     if (over && !have) break;
 

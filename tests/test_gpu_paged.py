@@ -405,6 +405,60 @@ def test_chunks_on_two_streams_at_once(d):
             assert torch.equal(o, want[i][0]) and torch.equal(z, want[i][1])
 
 
+def test_chunk_graphs_with_their_own_workspaces_replay_side_by_side(d):
+    cs = [Chunk(d, f, 64, 32, [(2, 1500), (5, 300), (1, 40)], seed=20 + i)
+          for i, f in enumerate(FORMATS)]
+    runs = []
+    for c in cs:
+        out = torch.empty(c.T, 32, 512, dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty(c.T, 32, device="cuda")
+        ws = c.kv.workspace(c.T, 3, 32)
+        want = [x.clone() for x in c.run(out=out, lse=lse, ws=ws)]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run(out=out, lse=lse, ws=ws)
+        runs.append((g, out, lse, ws, want))
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(5):
+        for _, out, lse, _, _ in runs:
+            out.fill_(7)
+            lse.fill_(7)
+        torch.cuda.synchronize()
+        for (g, *_), s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                for _ in range(3):
+                    g.replay()
+        torch.cuda.synchronize()
+        for _, out, lse, _, want in runs:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_chunk_more_requests_than_threads(d, fmt):
+    # 1100 requests, every third without a token, every fifth without a context
+    reqs = [(0 if i % 3 == 0 else 1 + i % 2, 0 if i % 5 == 0 else 1 + i * 37 % 290)
+            for i in range(1100)]
+    c = Chunk(d, fmt, 32, 8, reqs, seed=21)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_chunk_wait_that_runs_out_reports_and_recovers(d, fmt):
+    # with a limit of 1 ns the waits give up at once: the call reports it, lets
+    # its copies land, frees its tensor memory, and the next call computes
+    c = Chunk(d, fmt, 64, 128, [(1, 3000), (9, 500)], seed=22)
+    d.ts_set_wait_limit_ns(1)
+    try:
+        c.run()
+        bits = c.kv.synchronize()
+    finally:
+        d.ts_set_wait_limit_ns(0)
+    assert bits == d._abi.TS_DEVERR_TIMEOUT
+    for _ in range(2):
+        c.check(*c.run())
+
+
 def test_cache_past_32_bit_offsets(d):
     # slots whose byte offsets (and 16-byte offsets) pass 2^32
     rng = np.random.default_rng(14)
