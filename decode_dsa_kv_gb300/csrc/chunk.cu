@@ -56,10 +56,10 @@ struct Layout {
   static constexpr int kLoaders = k8 ? kConvertWarps + 1 : kTmaWarps;
   static constexpr int kMmaWarp = kSoftmaxWarps + kLoaders;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
-  static constexpr int kStages = k8 ? 4 : 7;
+  static constexpr int kStages = k8 ? 5 : 7;
   static constexpr uint32_t kRawBytes = k8 ? kConvertWarps * kRawUnit : 0;
   static constexpr uint32_t kSmem =
-      kBarBytes + 1024 + kQBytes + kPBytes + kStages * kStageBytes + kRawBytes;
+      kQBytes + kPBytes + kStages * kStageBytes + kRawBytes + kBarBytes;
   static_assert(kSmem <= 227 * 1024, "dynamic shared memory of one CTA");
   // Registers a thread after the split: the softmax's warpgroups take what the
   // others give back (of 384 x 168, or 512 x 128, at launch).
@@ -91,7 +91,6 @@ struct Bars {
   uint64_t p_full;          // even CTA: P written and S read in both CTAs
   uint64_t pv_done;         // both: a tile's value products are complete
   uint64_t raw[kConvertWarps];  // a converting warp's unit of codes
-  uint64_t q_raw;                  // Q as loaded (8-bit rows: reordered before use)
   uint64_t drain;
   uint64_t sum[16];
   uint32_t tmem_slot;
@@ -355,37 +354,24 @@ __device__ __forceinline__ uint4 scaled(const uint4& x, float f) {
   return make_uint4(mul(x.x), mul(x.y), mul(x.z), mul(x.w));
 }
 
-// 16 e4m3 codes times 2^-120 f as bf16 values, each four in the order 0, 2, 1,
-// 3 (f is 2^120 times the codes' scale). A code's sign, exponent and mantissa
-// bits are moved into a bf16's places; a subnormal code becomes a bf16
-// subnormal of the same value, so no code is special but NaN (which the cache
-// may not hold below ctx_len). 9 instructions for four codes; through the
-// conversions to half and float it is 12. The order costs nothing: Q's latent
-// part is laid out alike, and the epilogue names the output's registers alike.
+// 16 e4m3 codes times 2^-120 f as bf16 values (f is 2^120 times the codes'
+// scale). Two codes are spread over a word's halves, each below copies of its
+// sign; shifted by 4 and masked, sign, exponent and mantissa bits lie in a
+// bf16's places. A subnormal code becomes a bf16 subnormal of the same value,
+// so no code is special but NaN (which the cache may not hold below ctx_len).
+// 8 instructions for four codes; through the conversions to half and float it
+// is 12.
 __device__ __forceinline__ void widen_codes(const uint4& c, float f, uint4 (&o)[2]) {
-  auto even = [](uint32_t w) { return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u); };
-  auto odd = [](uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u); };
-  o[0] = scaled(make_uint4(even(c.x), odd(c.x), even(c.y), odd(c.y)), f);
-  o[1] = scaled(make_uint4(even(c.z), odd(c.z), even(c.w), odd(c.w)), f);
-}
-
-// 8 bf16 values, each four in the order of widen_codes.
-__device__ __forceinline__ uint4 code_order(const uint4& x) {
-  return make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632),
-                    __byte_perm(x.z, x.w, 0x5410), __byte_perm(x.z, x.w, 0x7632));
-}
-
-// O's dims from the order of widen_codes back to their own.
-template <int kFmt>
-__device__ __forceinline__ void natural_order(uint32_t (&v)[32]) {
-  if (kFmt == DSA_CACHE_E4M3) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      const uint32_t x = v[i + 1];
-      v[i + 1] = v[i + 2];
-      v[i + 2] = x;
-    }
-  }
+  // (bit 3 of a byte's selector takes its sign in all eight bits)
+  auto spread = [](uint32_t w, uint32_t bytes) {
+    uint32_t x;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(x) : "r"(w), "r"(bytes));
+    return (x << 4) & 0x87f087f0u;
+  };
+  auto low = [&](uint32_t w) { return spread(w, 0x9180); };
+  auto high = [&](uint32_t w) { return spread(w, 0xb3a2); };
+  o[0] = scaled(make_uint4(low(c.x), high(c.x), low(c.y), high(c.y)), f);
+  o[1] = scaled(make_uint4(low(c.z), high(c.z), low(c.w), high(c.w)), f);
 }
 
 struct Maps {
@@ -604,11 +590,12 @@ __device__ __forceinline__ void load_q_8bit(Loader& ld, Walk walk) {
     if (qn > 0 && !ld.wait(&ld.bars->q_empty, (qn - 1) & 1)) break;
     const int row0 = sg.r.q0 * a.H + sg.row0;
     if (a.q_dense) {
-      ld.q_by_tma(row0, sg.rows, dsmem_addr(&ld.bars->q_raw, ld.rank));
+      ld.q_by_tma(row0, sg.rows, ld.q_full);
     } else {
       ld.q_by_copy(row0, sg.rows, 0, 1);
+      fence_proxy_async_smem();
       __syncwarp();
-      if (ld.el) mbar_arrive(&ld.bars->q_raw);
+      if (ld.el) mbar_arrive_cluster(ld.q_full);
     }
     ++qn;
   }
@@ -623,27 +610,27 @@ __device__ __forceinline__ void load_q_8bit(Loader& ld, Walk walk) {
 // at half rate, 32 units a tile.
 __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
   constexpr int kStages = Layout<DSA_CACHE_E4M3>::kStages;
-  static_assert(kStages == 4, "a unit's place is (number / 2) % 4");
-  static_assert((kConvertWarps + 1) / 2 <= 2 * kStages, "wait_free");
+  static_assert(kConvertWarps == 2 * kStages, "a warp's units all go to one place");
   const Args& a = ld.a;
   Bars* bars = ld.bars;
   const int lane = ld.lane;
   uint8_t* raw = ld.raw + w * kRawUnit;
   uint64_t* raw_bar = &bars->raw[w];
+  const uint32_t at = w >> 1, half = w & 1, bar = ld.full + at * 8;
+  uint8_t* dst = ld.ring + at * kStageBytes + half * kVBox;
   const uint32_t read = lane * 64, read_x = (lane >> 1 & 3) << 4;
   const uint32_t write = lane * 128, write_x = (lane & 7) << 4;
   // the unit in flight: its number, its keys of the context, its valid 16-key
-  // steps, whether it is rope, whether Q comes before it; its slots; its scales
-  bool have = false, rope = false, first = false;
-  uint32_t number = 0, valid = 0;
+  // steps, whether it is rope; its slots; its scales
+  bool have = false, rope = false;
+  uint32_t wrap = 0, valid = 0;
   int count = 0, unit_slots = -1;
   float scale0 = 0.f, scale1 = 0.f;
-  uint32_t landed = 0, qn = 0;
+  uint32_t landed = 0;
   // the walk: this warp's next unit is number i of the phase's n
   Segment sg;
-  bool inside = false, fresh = false, over = false;
+  bool inside = false, over = false;
   int t = 0, i = w, n = 0, here = -1, now = -1, next = -1;
-  uint32_t next_number = w;
   for (;;) {
     while (!over && i >= n) {  // on to the phase that holds the next unit
       i -= n;
@@ -655,7 +642,7 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
       if (!inside) {
         over = !walk.next(a, sg);
         if (over) break;
-        inside = fresh = true;
+        inside = true;
         t = sg.t0;
         here = -1;
         now = ld.slots_of(sg, t, ld.pages_of(sg, t));
@@ -696,8 +683,8 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
       int v = i >> 1, step, kb;
       if (t < sg.t1 && v < kBlocks) {
         slots = now;
-        step = ld.rank * 8 + (i & 1) * 4;
-        next_count = sg.r.ctx - t * kKeys - int(ld.rank) * 128 - (i & 1) * 64;
+        step = ld.rank * 8 + half * 4;
+        next_count = sg.r.ctx - t * kKeys - int(ld.rank) * 128 - half * 64;
         kb = v;
         next_rope = v == kBlocks - 1;
       } else {
@@ -705,7 +692,7 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
         slots = here;
         step = (v >> 1) * 4;
         next_count = sg.r.ctx - (t - 1) * kKeys - (v >> 1) * 64;
-        kb = ld.rank * 4 + (v & 1) * 2 + (i & 1);
+        kb = ld.rank * 4 + (v & 1) * 2 + half;
       }
       next_count = min(max(next_count, 0), 64);
       next_valid = __ballot_sync(0xffffffffu, slots >= 0) >> step & 15;
@@ -713,16 +700,14 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
       slots = __shfl_sync(0xffffffffu, slots, (step + lane) & 31);
       if (!next_rope) {
         const uint32_t boxes = next_valid & (ld.v_step == 4 ? 1u : ld.v_step == 2 ? 5u : 15u);
-        int at[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) at[k] = __shfl_sync(0xffffffffu, slots, k);
         if (ld.el) {
           if (boxes) mbar_expect_tx(raw_bar, __popc(boxes) * ld.v_step * 1024);
           else mbar_arrive(raw_bar);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (boxes >> k & 1)
-              tma_load_3d(raw + k * 1024, &ld.maps.code, raw_bar, kb * 64, at[k], 0);
+        }
+#pragma unroll 1
+        for (int k = 0; k < 4; k += ld.v_step) {
+          const int at = __shfl_sync(0xffffffffu, slots, k);
+          if (ld.el && at >= 0) tma_load_3d(raw + k * 1024, &ld.maps.code, raw_bar, kb * 64, at, 0);
         }
         // (without a condition, which would wait for the values here)
         const int slot0 = max(__shfl_sync(0xffffffffu, slots, lane >> 4), 0) + (lane & 15);
@@ -735,21 +720,7 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
 
     // the unit in flight: into its place
     if (have) {
-      const uint32_t at = number >> 1 & 3, half = number & 1, bar = ld.full + at * 8;
-      if (first) {  // Q's latent part into the codes' order
-        if (!ld.wait(&bars->q_raw, qn & 1)) break;
-        ++qn;
-#pragma unroll 2
-        for (int k = w * 32 + lane; k < kRowsCta * 64; k += kConvertWarps * 32) {
-          uint4* x = reinterpret_cast<uint4*>(ld.q_tile) + k;
-          *x = code_order(*x);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (ld.el) mbar_arrive_cluster(ld.q_full);
-      }
-      if (!ld.wait_free(at, number >> 3)) break;
-      uint8_t* dst = ld.ring + at * kStageBytes + half * kVBox;
+      if (!ld.wait_free(at, wrap++)) break;
       if (rope) {  // bf16 as it is, by TMA
         const uint32_t boxes = valid & (ld.v_step == 4 ? 1u : ld.v_step == 2 ? 5u : 15u);
         if (ld.el) mbar_expect_tx_cluster(bar, __popc(boxes) * ld.v_step * 2048);
@@ -759,20 +730,24 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
           if (slot >= 0 && ld.el) tma_load_3d_pair(dst + k * 2048, &ld.maps.k, bar, 0, slot, 0);
         }
       } else {
-        // 2^120 scale is past bf16's range for a scale above 2^7
+        // (2^120 scale is past bf16's range for a scale above 2^7: those codes
+        // get their scale in a second product)
         const bool big = __any_sync(0xffffffffu, fmaxf(f0, f1) > 128.f);
+        const float g0 = big ? 0x1p120f : f0 * 0x1p120f, g1 = big ? 0x1p120f : f1 * 0x1p120f;
+        auto place = [&](int k) -> uint4* {
+          return reinterpret_cast<uint4*>(dst + write + (k >> 3) * 4096 +
+                                          (((k & 7) << 4) ^ write_x));
+        };
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float f = k < 4 ? f0 : f1;
           uint4 o[2];
-          widen_codes(code[k], big ? 0x1p120f : f * 0x1p120f, o);
-          if (big) {
-            o[0] = scaled(o[0], f);
-            o[1] = scaled(o[1], f);
-          }
-          uint8_t* row = dst + write + (k >> 2) * 4096;
-          *reinterpret_cast<uint4*>(row + (((k & 3) << 5) ^ write_x)) = o[0];
-          *reinterpret_cast<uint4*>(row + ((((k & 3) << 5) + 16) ^ write_x)) = o[1];
+          widen_codes(code[k], k < 4 ? g0 : g1, o);
+          *place(2 * k) = o[0];
+          *place(2 * k + 1) = o[1];
+        }
+        if (big) {
+#pragma unroll 1
+          for (int k = 0; k < 16; ++k) *place(k) = scaled(*place(k), k < 8 ? f0 : f1);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -781,13 +756,9 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
     }
     have = !over;
     rope = next_rope;
-    first = fresh;
-    fresh = false;
-    number = next_number;
     valid = next_valid;
     count = next_count;
     unit_slots = slots;
-    next_number += kConvertWarps;
     i += kConvertWarps;
   }
 }
@@ -799,12 +770,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
   constexpr int kStages = Lay::kStages, kMmaWarp = Lay::kMmaWarp;
   constexpr int kSoftmaxWarps = Lay::kSoftmaxWarps, kParts = Lay::kParts;
   constexpr int kCols = 128 / kParts;  // score columns of a softmax thread
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  Bars* bars = reinterpret_cast<Bars*>(smem_raw);
-  uint8_t* q_tile = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + kBarBytes + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t q_tile[];  // (swizzled tiles: 1024-byte aligned)
   uint8_t* p_tile = q_tile + kQBytes;
   uint8_t* ring = p_tile + kPBytes;
+  uint8_t* raw = ring + kStages * kStageBytes;
+  Bars* bars = reinterpret_cast<Bars*>(raw + Lay::kRawBytes);
   volatile int* abort = &bars->abort;
   const int pair = blockIdx.x >> 1;
   const uint32_t rank = cluster_ctarank();
@@ -823,14 +793,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
       mbar_init(&bars->empty[0][s], 1);
       mbar_init(&bars->empty[1][s], 1);
     }
-    mbar_init(&bars->q_full, Lay::k8 ? 2 * kConvertWarps : a.q_dense ? 2 : 2 * kTmaWarps);
+    mbar_init(&bars->q_full, Lay::k8 || a.q_dense ? 2 : 2 * kTmaWarps);
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->s_full[0], 1);
     mbar_init(&bars->s_full[1], 1);
     mbar_init(&bars->p_full, 2 * Lay::kSoftmaxWarps);
     mbar_init(&bars->pv_done, 1);
     for (int i = 0; i < kConvertWarps; ++i) mbar_init(&bars->raw[i], 1);
-    mbar_init(&bars->q_raw, 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     mbar_fence_init();
@@ -978,7 +947,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
       uint8_t* dst = direct ? reinterpret_cast<uint8_t*>(a.out) + (grow - r) * (DSA_DV * 2)
                             : reinterpret_cast<uint8_t*>(a.opart) +
                                   (int64_t(slot) * a.part_rows + rr - r) * (DSA_DV * 4);
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool empty = l == 0.f;  // no key (a NaN is kept)
+      const float inv = empty ? 0.f : 1.f / l;
       const int mine = min(kRowsCta, sg.rows - int(rank) * kRowsCta);  // rows to store
 #pragma unroll 1
       for (int pass = 0; pass < (direct ? 2 : 4); ++pass) {
@@ -996,13 +966,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
             for (int h = 0; h < 2; ++h) {
               tmem_ld32(col + pass * 64 + h * 32, v);
               tmem_wait_ld();
-              natural_order<kFmt>(v);
               uint32_t o[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 // (a row without a key has no O: zeros, whatever lies there)
-                const float x0 = l > 0.f ? __uint_as_float(v[2 * i]) * inv : 0.f;
-                const float x1 = l > 0.f ? __uint_as_float(v[2 * i + 1]) * inv : 0.f;
+                const float x0 = empty ? 0.f : __uint_as_float(v[2 * i]) * inv;
+                const float x1 = empty ? 0.f : __uint_as_float(v[2 * i + 1]) * inv;
                 const __nv_bfloat162 h2 = __floats2bfloat162_rn(x0, x1);
                 o[i] = *reinterpret_cast<const uint32_t*>(&h2);
               }
@@ -1013,7 +982,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
           } else {
             tmem_ld32(col + pass * 32, v);
             tmem_wait_ld();
-            natural_order<kFmt>(v);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               put(j, make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
@@ -1030,26 +998,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
       }
       if (valid && half == 0 && part == 0) {
         if (!direct) a.ml[int64_t(slot) * a.part_rows + rr] = make_float2(m, l);
-        else if (a.lse) a.lse[grow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        else if (a.lse) a.lse[grow] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
       }
       if (!direct && rank == 0 && threadIdx.x == 0)
         a.meta[slot] = make_int4(static_cast<int>(int64_t(sg.r.q0) * a.H + sg.row0), sg.rows,
                                  (sg.starts ? kStarts : 0) | (sg.ends ? kEnds : 0), 0);
       tc_fence_before();
     }
-  } else if (warp < kMmaWarp) {
-    // ---------------- loaders: Q, and the K and V stages in turn ----------------
-    regs_dec<Lay::kOtherRegs>();
-    const int w = warp - kSoftmaxWarps, k_step = min(8, (1 << a.page_shift) >> 4);
-    Loader ld{a, maps, bars, q_tile, ring, ring + kStages * kStageBytes, rank,
-              dsmem_addr(&bars->q_full, 0), dsmem_addr(&bars->full[0], 0), lane, elect_one(),
-              abort, k_step, min(4, k_step)};
-    if (!Lay::k8) load_bf16(ld, walk, w);
-    else if (w == kConvertWarps) load_q_8bit(ld, walk);
-    else load_codes(ld, walk, w);
   } else {
-    regs_dec<Lay::kOtherRegs>();
-    if (rank == 0) {
+    regs_dec<Lay::kOtherRegs>();  // (one instruction for all of a warpgroup's warps)
+    if (warp < kMmaWarp) {
+      // ---------------- loaders: Q, and the K and V stages in turn ----------------
+      const int w = warp - kSoftmaxWarps, k_step = min(8, (1 << a.page_shift) >> 4);
+      Loader ld{a, maps, bars, q_tile, ring, raw, rank,
+                dsmem_addr(&bars->q_full, 0), dsmem_addr(&bars->full[0], 0), lane, elect_one(),
+                abort, k_step, min(4, k_step)};
+      if (!Lay::k8) load_bf16(ld, walk, w);
+      else if (w == kConvertWarps) load_q_8bit(ld, walk);
+      else load_codes(ld, walk, w);
+    } else if (rank == 0) {
       // ---------------- MMA issuer (the even CTA's, for both) ----------------
       // a negative scale negates Q (its bit of the instruction descriptor)
       const uint32_t id_s =
@@ -1207,7 +1174,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Arg
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t row = int64_t(head.x) + r;
   uint2* dst = reinterpret_cast<uint2*>(a.out + row * DSA_DV) + lane;
 #pragma unroll
@@ -1217,7 +1184,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Arg
     dst[32 * c] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
                              *reinterpret_cast<const uint32_t*>(&hi));
   }
-  if (lane == 0 && a.lse) a.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+  if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -303,6 +303,35 @@ def test_chunk_strided_queries_and_untouched_rows(d, fmt):
     assert torch.all(out[9:] == 3) and torch.all(lse[9:] == 5)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("ctx", [200, 9000])   # a row tile by itself; one that is joined
+def test_chunk_a_nan_in_a_query_stays_in_its_row(d, fmt, ctx):
+    c = Chunk(d, fmt, 64, 20, [(3, ctx)], seed=23)
+    want, want_lse = [x.clone() for x in c.run()]
+    c.q[1, 7, 100] = math.nan
+    out, lse = c.run()
+    assert c.kv.synchronize() == 0
+    row = torch.zeros(3, 20, dtype=torch.bool, device="cuda")
+    row[1, 7] = True
+    assert torch.all(torch.isnan(out[row])) and torch.all(torch.isnan(lse[row]))
+    assert torch.equal(out[~row], want[~row]) and torch.equal(lse[~row], want_lse[~row])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_chunk_large_and_small_latent_groups(d, fmt):
+    # groups of 128 whose scales lie far apart: 2^13 and more beside 2^-40 (the
+    # scores' weights fall on the last group and the rope part)
+    def rows(rng, n):
+        x = bf16_bits_to_f64(random_rows(rng, n))
+        x[:, :128] *= 2.0 ** 20
+        x[:, 128:256] *= 2.0 ** -40
+        return round_to_bf16_bits(x)
+    c = Chunk(d, fmt, 64, 16, [(3, 700), (1, 70)], seed=24, rows=rows)
+    c.q64[:, :, :128] = 0
+    c.q[:, :, :128] = 0
+    c.check(*c.run())
+
+
 def test_chunk_without_lse(d):
     c = Chunk(d, "bf16", 64, 16, [(3, 200)], seed=6)
     want, lse = c.run()
