@@ -42,30 +42,32 @@ constexpr uint32_t kStageBytes = 16384;  // K: 128 keys x 64 dims; V: 64 keys x 
 constexpr uint32_t kVBox = 64 * 128;     // V: 64 keys x 64 dims
 constexpr uint32_t kBarBytes = 3072;
 // Warp roles. bf16 rows: warps 0..7 softmax, 8..10 load by TMA (every third
-// stage each), 11 issues the products. 8-bit rows: warps 0..3 softmax, 4..13
-// convert (every tenth half of a stage each), 14 loads Q, 15 issues the
-// products: the conversion's integer instructions, not the softmax, are what
-// this kernel has most of.
-constexpr int kTmaWarps = 3, kConvertWarps = 10;
+// stage each), 11 issues the products. 8-bit rows: warps 0..3 softmax, 4..11
+// convert (every eighth half of a stage each), 12 walks the work for them and
+// loads Q, 15 issues the products; 13 and 14 fill the warpgroup.
+constexpr int kTmaWarps = 3, kConvertWarps = 8;
+constexpr int kPhases = 3;  // 8-bit rows: phase records on their way to the converting warps
 constexpr uint32_t kRawUnit = 4096;  // 64 keys x 64 codes
 template <int kFmt>
 struct Layout {
   static constexpr bool k8 = kFmt == DSA_CACHE_E4M3;
   static constexpr int kSoftmaxWarps = k8 ? 4 : 8;
   static constexpr int kParts = kSoftmaxWarps / 4;  // threads of a TMEM lane
-  static constexpr int kLoaders = k8 ? kConvertWarps + 1 : kTmaWarps;
+  static constexpr int kLoaders = k8 ? kConvertWarps + 3 : kTmaWarps;
   static constexpr int kMmaWarp = kSoftmaxWarps + kLoaders;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
-  static constexpr int kStages = k8 ? 5 : 7;
+  static constexpr int kStages = k8 ? 4 : 7;
   static constexpr uint32_t kRawBytes = k8 ? kConvertWarps * kRawUnit : 0;
   static constexpr uint32_t kSmem =
       kQBytes + kPBytes + kStages * kStageBytes + kRawBytes + kBarBytes;
   static_assert(kSmem <= 227 * 1024, "dynamic shared memory of one CTA");
   // Registers a thread after the split: the softmax's warpgroups take what the
-  // others give back (of 384 x 168, or 512 x 128, at launch).
-  static constexpr int kSoftmaxRegs = k8 ? 224 : 200, kOtherRegs = k8 ? 96 : 104;
-  static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + (kThreads - 32 * kSoftmaxWarps) * kOtherRegs <=
-                    kThreads * (k8 ? 128 : 168), "register split");
+  // others (the converting warps, the last warpgroup) give back, of 384 x 168,
+  // or 512 x 128, at launch.
+  static constexpr int kSoftmaxRegs = k8 ? 248 : 200, kConvertRegs = 104, kLastRegs = k8 ? 56 : 104;
+  static constexpr int kConvertThreads = kThreads - 32 * kSoftmaxWarps - 128;
+  static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + kConvertThreads * kConvertRegs +
+                        128 * kLastRegs <= kThreads * (k8 ? 128 : 168), "register split");
 };
 constexpr int kMaxStages = 7;
 constexpr int kMaxPairs = 80;
@@ -80,6 +82,15 @@ constexpr float kLn2 = 0.6931471805599453f;
 // sums no precision, and O is seldom rescaled.
 constexpr float kSlack = 8.f;
 
+// 8-bit rows: what the converting warps need to know of a phase (a key tile's
+// K units and the V units of the tile before it).
+struct Phase {
+  int slot[16];  // of the tile's 16-key steps
+  int units;     // of the phase; -1: no more
+  int k_units;   // the first of them
+  int rest;      // keys of the context from the tile on
+};
+
 struct Bars {
   uint64_t full[kMaxStages];   // even CTA: a stage's parts in both CTAs have landed
   // both: the products reading the stage are done; a place's uses alternate
@@ -90,6 +101,8 @@ struct Bars {
   uint64_t s_full[2];       // both: a tile's scores are complete
   uint64_t p_full;          // even CTA: P written and S read in both CTAs
   uint64_t pv_done;         // both: a tile's value products are complete
+  uint64_t phase_full[kPhases], phase_empty[kPhases];
+  Phase phase[kPhases];
   uint64_t raw[kConvertWarps];  // a converting warp's unit of codes
   uint64_t drain;
   uint64_t sum[16];
@@ -581,24 +594,53 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
   }
 }
 
-// 8-bit rows: Q of every row tile.
+// 8-bit rows: walks the pair's work for the converting warps, which have too
+// few registers for it (what they spill comes back at L2's distance: nearly all
+// of the L1 is shared memory here), and loads Q.
 __device__ __forceinline__ void load_q_8bit(Loader& ld, Walk walk) {
   const Args& a = ld.a;
+  Bars* bars = ld.bars;
   Segment sg;
-  uint32_t qn = 0;
-  while (walk.next(a, sg)) {
-    if (qn > 0 && !ld.wait(&ld.bars->q_empty, (qn - 1) & 1)) break;
-    const int row0 = sg.r.q0 * a.H + sg.row0;
-    if (a.q_dense) {
-      ld.q_by_tma(row0, sg.rows, ld.q_full);
-    } else {
-      ld.q_by_copy(row0, sg.rows, 0, 1);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (ld.el) mbar_arrive_cluster(ld.q_full);
+  uint32_t qn = 0, at = 0, wrap = 0;
+  bool ok = true;
+  auto publish = [&](int slots, int units, int k_units, int rest) {
+    if (wrap > 0) ok = ld.wait(&bars->phase_empty[at], (wrap - 1) & 1);
+    if (!ok) return;
+    Phase& p = bars->phase[at];
+    if (ld.lane < 16) p.slot[ld.lane] = slots;
+    if (ld.lane == 16) p.units = units;
+    if (ld.lane == 17) p.k_units = k_units;
+    if (ld.lane == 18) p.rest = rest;
+    __syncwarp();
+    if (ld.el) mbar_arrive(&bars->phase_full[at]);
+    if (++at == kPhases) at = 0, ++wrap;
+  };
+  while (ok && walk.next(a, sg)) {
+    int page = ld.pages_of(sg, sg.t0);
+#pragma unroll 1
+    for (int t = sg.t0; t <= sg.t1 && ok; ++t) {
+      const int slots = ld.slots_of(sg, t, page);
+      page = ld.pages_of(sg, t + 1);
+      publish(slots, 2 * stages_of(sg, t), t < sg.t1 ? 2 * kBlocks : 0, sg.r.ctx - t * kKeys);
+      if (t > sg.t0 || !ok) continue;
+      // Q, behind the first phase: a converting warp asks for its next unit's
+      // phase before it places a unit of the row tile before, and that tile's
+      // last score products wait for those
+      if (qn > 0) ok = ld.wait(&bars->q_empty, (qn - 1) & 1);
+      if (!ok) break;
+      ++qn;
+      const int row0 = sg.r.q0 * a.H + sg.row0;
+      if (a.q_dense) {
+        ld.q_by_tma(row0, sg.rows, ld.q_full);
+      } else {
+        ld.q_by_copy(row0, sg.rows, 0, 1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ld.el) mbar_arrive_cluster(ld.q_full);
+      }
     }
-    ++qn;
   }
+  if (ok) publish(-1, -1, 0, 0);
 }
 
 // 8-bit rows: warp w of kConvertWarps. A stage is two units, its halves of 64
@@ -606,10 +648,15 @@ __device__ __forceinline__ void load_q_8bit(Loader& ld, Walk walk) {
 // i + 32. A unit's codes come by TMA (64-byte swizzle: the lanes' reads of one
 // piece of every row meet no bank twice) into the warp's raw space; once they
 // are in registers the next unit's are sent for, and land while this one is
-// converted. The integer pipe bounds this: some 230 of its instructions a unit
-// at half rate, 32 units a tile.
-__device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
+// converted. What bounds this kernel is the shared memory's bandwidth: a tile's
+// codes written and read, its bf16 values written and read by the products are
+// some 9600 clocks of it, of 10,100 a tile (the products alone take 4556; ten
+// converting warps or a ring of five stages give the same time as eight and
+// four, and codes by plain loads into registers 1095 against 850 us at 4 x 500
+// tokens of an earlier step).
+__device__ __forceinline__ void load_codes(Loader& ld, int w) {
   constexpr int kStages = Layout<DSA_CACHE_E4M3>::kStages;
+  static_assert(kConvertWarps <= 2 * kBlocks, "every warp has a unit of a row tile's first phase");
   static_assert(kConvertWarps == 2 * kStages, "a warp's units all go to one place");
   const Args& a = ld.a;
   Bars* bars = ld.bars;
@@ -620,36 +667,36 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
   uint8_t* dst = ld.ring + at * kStageBytes + half * kVBox;
   const uint32_t read = lane * 64, read_x = (lane >> 1 & 3) << 4;
   const uint32_t write = lane * 128, write_x = (lane & 7) << 4;
-  // the unit in flight: its number, its keys of the context, its valid 16-key
-  // steps, whether it is rope; its slots; its scales
+  // the unit in flight: whether it is rope, its valid 16-key steps, its keys of
+  // the context, its slots and scales
   bool have = false, rope = false;
   uint32_t wrap = 0, valid = 0;
   int count = 0, unit_slots = -1;
   float scale0 = 0.f, scale1 = 0.f;
   uint32_t landed = 0;
-  // the walk: this warp's next unit is number i of the phase's n
-  Segment sg;
-  bool inside = false, over = false;
-  int t = 0, i = w, n = 0, here = -1, now = -1, next = -1;
+  // this warp's next unit is number i of the phase's n, of which the first
+  // k_units are K's; the slots and keys of the phase's tile and the one before
+  bool over = false;
+  int i = w, n = 0, k_units = 0, here = -1, now = -1, rest_here = 0, rest = 0;
+  uint32_t ph = 0, ph_parity = 0;
   for (;;) {
-    while (!over && i >= n) {  // on to the phase that holds the next unit
+    bool ok = true;
+    while (ok && !over && i >= n) {  // on to the phase that holds the next unit
       i -= n;
-      if (inside) {
-        here = now;
-        now = next;
-        inside = ++t <= sg.t1;
-      }
-      if (!inside) {
-        over = !walk.next(a, sg);
-        if (over) break;
-        inside = true;
-        t = sg.t0;
-        here = -1;
-        now = ld.slots_of(sg, t, ld.pages_of(sg, t));
-      }
-      n = 2 * stages_of(sg, t);
-      next = ld.slots_of(sg, t + 1, ld.pages_of(sg, t + 1));
+      here = now;
+      rest_here = rest;
+      ok = ld.wait(&bars->phase_full[ph], ph_parity);
+      const Phase& p = bars->phase[ph];
+      n = p.units;
+      k_units = p.k_units;
+      rest = p.rest;
+      now = lane < 16 ? p.slot[lane] : -1;
+      over = n < 0;
+      __syncwarp();
+      if (ld.el) mbar_arrive(&bars->phase_empty[ph]);
+      if (++ph == kPhases) ph = 0, ph_parity ^= 1;
     }
+    if (!ok) break;
     if (over && !have) break;
 
     // the unit in flight: its codes into registers
@@ -681,17 +728,17 @@ __device__ __forceinline__ void load_codes(Loader& ld, Walk walk, int w) {
     int next_count = 0, slots = -1;
     if (!over) {
       int v = i >> 1, step, kb;
-      if (t < sg.t1 && v < kBlocks) {
+      if (i < k_units) {
         slots = now;
         step = ld.rank * 8 + half * 4;
-        next_count = sg.r.ctx - t * kKeys - int(ld.rank) * 128 - half * 64;
+        next_count = rest - int(ld.rank) * 128 - int(half) * 64;
         kb = v;
         next_rope = v == kBlocks - 1;
       } else {
-        v -= t < sg.t1 ? kBlocks : 0;  // 64-key group v / 2, dims half v % 2
+        v -= k_units >> 1;  // 64-key group v / 2, dims half v % 2
         slots = here;
         step = (v >> 1) * 4;
-        next_count = sg.r.ctx - (t - 1) * kKeys - (v >> 1) * 64;
+        next_count = rest_here - (v >> 1) * 64;
         kb = ld.rank * 4 + (v & 1) * 2 + half;
       }
       next_count = min(max(next_count, 0), 64);
@@ -800,6 +847,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
     mbar_init(&bars->p_full, 2 * Lay::kSoftmaxWarps);
     mbar_init(&bars->pv_done, 1);
     for (int i = 0; i < kConvertWarps; ++i) mbar_init(&bars->raw[i], 1);
+    for (int i = 0; i < kPhases; ++i) {
+      mbar_init(&bars->phase_full[i], 1);
+      mbar_init(&bars->phase_empty[i], kConvertWarps);
+    }
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     mbar_fence_init();
@@ -815,6 +866,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
   tc_fence_after();
   const uint32_t tmem = bars->tmem_slot;
 
+  auto make_loader = [&]() -> Loader {
+    const int k_step = min(8, (1 << a.page_shift) >> 4);
+    return Loader{a, maps, bars, q_tile, ring, raw, rank, dsmem_addr(&bars->q_full, 0),
+                  dsmem_addr(&bars->full[0], 0), lane, elect_one(), abort, k_step, min(4, k_step)};
+  };
   Walk walk(bars);
   Segment sg;
   if (warp < kSoftmaxWarps) {
@@ -1005,17 +1061,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
                                  (sg.starts ? kStarts : 0) | (sg.ends ? kEnds : 0), 0);
       tc_fence_before();
     }
+  } else if (Lay::k8 && warp < kSoftmaxWarps + kConvertWarps) {
+    // ---------------- 8-bit rows: the K and V stages ----------------
+    regs_dec<Lay::kConvertRegs>();
+    const int w = warp - kSoftmaxWarps;
+    Loader ld = make_loader();
+    load_codes(ld, w);
   } else {
-    regs_dec<Lay::kOtherRegs>();  // (one instruction for all of a warpgroup's warps)
+    // (one instruction for all of a warpgroup's warps)
+    regs_dec<Lay::kLastRegs>();
     if (warp < kMmaWarp) {
-      // ---------------- loaders: Q, and the K and V stages in turn ----------------
-      const int w = warp - kSoftmaxWarps, k_step = min(8, (1 << a.page_shift) >> 4);
-      Loader ld{a, maps, bars, q_tile, ring, raw, rank,
-                dsmem_addr(&bars->q_full, 0), dsmem_addr(&bars->full[0], 0), lane, elect_one(),
-                abort, k_step, min(4, k_step)};
-      if (!Lay::k8) load_bf16(ld, walk, w);
-      else if (w == kConvertWarps) load_q_8bit(ld, walk);
-      else load_codes(ld, walk, w);
+      // ---------------- Q; bf16 rows: the K and V stages ----------------
+      Loader ld = make_loader();
+      if (!Lay::k8) load_bf16(ld, walk, warp - kSoftmaxWarps);
+      else if (warp == kSoftmaxWarps + kConvertWarps) load_q_8bit(ld, walk);
     } else if (rank == 0) {
       // ---------------- MMA issuer (the even CTA's, for both) ----------------
       // a negative scale negates Q (its bit of the instruction descriptor)
