@@ -859,10 +859,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
     tmem_alloc_pair(&bars->tmem_slot, 512);
     tmem_relinquish_pair();
   }
+  // (the cluster meets over the plan: the barriers are there, and the tensor
+  // memory's address is read behind the plan's own barriers)
+  __syncwarp();
+  tc_fence_before();
+  cluster_arrive();
   if (blockIdx.x == 0) check_lengths(a);
   plan(a, bars, pair);
-  tc_fence_before();
-  cluster_sync_all();
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_slot;
 
@@ -1158,7 +1162,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (bars->abort) {
+  const bool aborted = bars->abort != 0;
+  if (aborted) {
     if (threadIdx.x == 0) report(a.err, TS_DEVERR_TIMEOUT);
     // copies in flight land, and every tcgen05 operation issued completes,
     // before the CTA may leave
@@ -1172,7 +1177,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
     }
     __syncthreads();
   }
-  cluster_sync_all();
+  // (relaxed: nobody here reads the sums on their way, and every arrival sent to
+  // the other CTA has been waited for, unless a wait gave up)
+  if (aborted) cluster_arrive();
+  else cluster_arrive_relaxed();
+  cluster_wait();
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
