@@ -61,10 +61,11 @@ struct Layout {
   static constexpr uint32_t kSmem =
       kQBytes + kPBytes + kStages * kStageBytes + kRawBytes + kBarBytes;
   static_assert(kSmem <= 227 * 1024, "dynamic shared memory of one CTA");
-  // Registers a thread after the split: the softmax's warpgroups take what the
-  // others (the converting warps, the last warpgroup) give back, of 384 x 168,
-  // or 512 x 128, at launch.
-  static constexpr int kSoftmaxRegs = k8 ? 248 : 200, kConvertRegs = 104, kLastRegs = k8 ? 56 : 104;
+  // Registers a thread after the split, of 384 x 168, or 512 x 128, at launch:
+  // such that little spills, because nearly all of the L1 is shared memory and
+  // what is spilled comes back at L2's distance (bf16 rows, 88 bytes spilled by
+  // the loaders at 104 registers: 2680 against 2540 us at 2048 x 128 over 8192).
+  static constexpr int kSoftmaxRegs = k8 ? 200 : 176, kConvertRegs = 104, kLastRegs = k8 ? 104 : 152;
   static constexpr int kConvertThreads = kThreads - 32 * kSoftmaxWarps - 128;
   static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + kConvertThreads * kConvertRegs +
                         128 * kLastRegs <= kThreads * (k8 ? 128 : 168), "register split");
@@ -932,31 +933,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
 #pragma unroll
           for (int k = 0; k < kParts; ++k) mx = fmaxf(mx, fmaxf(e[k][r], e[k][r + 64]));
         }
+        // the tile before this one is in O, and its P read. (Only now the weights:
+        // they go to P as they come, and the products are busy with the next
+        // tile's scores meanwhile. Held in registers over this wait they made the
+        // threads spill, and what is spilled comes back at L2's distance.)
+        if (ok && tg > 0) ok = mbar_warp_wait<false>(&bars->pv_done, (tg - 1) & 1, abort, wait_ns);
+        if (!ok) continue;  // the barrier above stays matched in every warp
         const bool moves = mx > m + kSlack;
         const float f = moves ? fast_exp2(m - mx) : 1.f;
         if (moves) m = mx;
-#pragma unroll
-        for (int k = 0; k < kCols / 64; ++k) l64[k] *= f;
-        const float mu = m == -INFINITY ? 0.f : m;
-        uint32_t packed[kCols / 2];
-        float l4[kCols / 64][4] = {};
-#pragma unroll
-        for (int i = 0; i < kCols / 2; ++i) {
-          const float p0 =
-              fast_exp2(fmaf(__uint_as_float(x[i >> 4][(2 * i) & 31]), a.scale_log2, -mu));
-          const float p1 =
-              fast_exp2(fmaf(__uint_as_float(x[i >> 4][(2 * i + 1) & 31]), a.scale_log2, -mu));
-          l4[i / 32][(2 * i) & 3] += p0;
-          l4[i / 32][(2 * i + 1) & 3] += p1;
-          const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
-          packed[i] = *reinterpret_cast<const uint32_t*>(&h2);
-        }
-#pragma unroll
-        for (int k = 0; k < kCols / 64; ++k)
-          l64[k] += (l4[k][0] + l4[k][1]) + (l4[k][2] + l4[k][3]);
-        // the tile before this one is in O, and its P read
-        if (ok && tg > 0) ok = mbar_warp_wait<false>(&bars->pv_done, (tg - 1) & 1, abort, wait_ns);
-        if (!ok) continue;  // the barrier above stays matched in every warp
         if (t > sg.t0 && __any_sync(0xffffffffu, moves)) {
           tc_fence_after();
           uint32_t v[32];
@@ -970,11 +955,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
           }
           tmem_wait_st();
         }
+        const float mu = m == -INFINITY ? 0.f : m;
         uint8_t* prow = p_tile + (half * 2 + part * (kCols / 64)) * kPBlock + r * 128;
 #pragma unroll
-        for (int j = 0; j < kCols / 8; ++j)
-          *reinterpret_cast<uint4*>(prow + (j >> 3) * kPBlock + (((j & 7) ^ (r & 7)) << 4)) =
-              make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+        for (int k = 0; k < kCols / 64; ++k) {
+          float l4[4] = {};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t packed[4];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const int c = k * 64 + j * 8 + i;
+              const float p0 = fast_exp2(fmaf(__uint_as_float(x[c >> 5][c & 31]), a.scale_log2, -mu));
+              const float p1 =
+                  fast_exp2(fmaf(__uint_as_float(x[c >> 5][(c & 31) + 1]), a.scale_log2, -mu));
+              l4[i & 3] += p0;
+              l4[(i & 3) + 1] += p1;
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+              packed[i / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            *reinterpret_cast<uint4*>(prow + k * kPBlock + ((j ^ (r & 7)) << 4)) =
+                make_uint4(packed[0], packed[1], packed[2], packed[3]);
+          }
+          l64[k] = l64[k] * f + ((l4[0] + l4[1]) + (l4[2] + l4[3]));
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
