@@ -649,12 +649,13 @@ __device__ __forceinline__ void load_q_8bit(Loader& ld, Walk walk) {
 // i + 32. A unit's codes come by TMA (64-byte swizzle: the lanes' reads of one
 // piece of every row meet no bank twice) into the warp's raw space; once they
 // are in registers the next unit's are sent for, and land while this one is
-// converted. What bounds this kernel is the shared memory's bandwidth: a tile's
-// codes written and read, its bf16 values written and read by the products are
-// some 9600 clocks of it, of 10,100 a tile (the products alone take 4556; ten
-// converting warps or a ring of five stages give the same time as eight and
-// four, and codes by plain loads into registers 1095 against 850 us at 4 x 500
-// tokens of an earlier step).
+// converted. What bounds this kernel is the shared memory's bandwidth: of some
+// 9500 clocks a tile, 5400 are wavefronts of its loads and stores (counted),
+// and the products' operands and the codes' arrival add about 4200; the
+// products by themselves take 4556. (Ten converting warps, or a ring of five
+// stages, take the same time as eight and four. Codes loaded straight into
+// registers, or widened before the wait for their place, took 1.2 to 1.5 times
+// as long: the warps then spilled.)
 __device__ __forceinline__ void load_codes(Loader& ld, int w) {
   constexpr int kStages = Layout<DSA_CACHE_E4M3>::kStages;
   static_assert(kConvertWarps <= 2 * kBlocks, "every warp has a unit of a row tile's first phase");

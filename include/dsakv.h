@@ -645,16 +645,23 @@ ts_status dsa_cache_read(const void* cache, int64_t num_slots, int fmt,
  *   ws    workspace of sfa_chunk_workspace_size(T, B, H) bytes, 256-byte
  *         aligned, contents need not be preserved; calls whose work may
  *         overlap on the GPU (two streams, two captured graphs) need one each
- * H <= 1024, T * H < 2^31 - 128, page_size a power of two in 16..1024. Cached
+ * H <= 1024, T * H < 2^31 - 128, num_slots < 2^31, page_size a power of two in
+ * 16..1024; the cache's pages are its num_slots / page_size whole ones. Cached
  * values below ctx_len must be finite (a NaN or an infinity there reaches the
- * outputs of every token of its tile); rows past ctx_len may hold anything.
+ * outputs of every token of its tile); rows past ctx_len may hold anything. A
+ * NaN or an infinity in q stays in its own row of out and lse.
  * bf16 products with fp32 accumulation, softmax statistics in fp32, the
- * softmax weights rounded to bf16 for the second product. T = 0 enqueues
- * nothing. cu_q out of order or past T sets TS_DEVERR_ORDER (taken as the
- * nearest valid value); a ctx_len below 0 or past table_stride * page_size
- * sets TS_DEVERR_CTX (taken as the nearest valid value); a page outside the
- * cache sets TS_DEVERR_SLOT_RANGE (the request's output is then undefined);
- * a wait that gave up sets TS_DEVERR_TIMEOUT.
+ * softmax weights rounded to bf16 for the second product; equal inputs give
+ * equal results, bit for bit. T = 0 enqueues nothing. Device errors:
+ *   TS_DEVERR_ORDER       cu_q out of order or past T (taken as the nearest
+ *                         valid value; requests that then share tokens leave
+ *                         those rows undefined)
+ *   TS_DEVERR_CTX         a ctx_len below 0, or past table_stride * page_size
+ *                         or 2^27 (taken as the nearest valid value)
+ *   TS_DEVERR_SLOT_RANGE  a page outside the cache (the request's output is
+ *                         then undefined)
+ *   TS_DEVERR_TIMEOUT     a wait gave up, after ts_set_wait_limit_ns's limit
+ *                         (2 s by default, 4 s at most): out is undefined
  * ------------------------------------------------------------------------- */
 size_t sfa_chunk_workspace_size(int T, int B, int H);
 ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_t* cu_q, int T, int B, int H,
