@@ -40,7 +40,7 @@ constexpr uint32_t kPBlock = kRowsCta * 128;     // 64 rows x 64 keys
 constexpr uint32_t kPBytes = 4 * kPBlock;        // 64 rows x 256 keys
 constexpr uint32_t kStageBytes = 16384;  // K: 128 keys x 64 dims; V: 64 keys x 2 x 64 dims
 constexpr uint32_t kVBox = 64 * 128;     // V: 64 keys x 64 dims
-constexpr uint32_t kBarBytes = 3072;
+constexpr uint32_t kBarBytes = 2944;
 // Warp roles. bf16 rows: warps 0..7 softmax, 8..10 load by TMA (every third
 // stage each), 11 issues the products. 8-bit rows: warps 0..3 softmax, 4..11
 // convert (every eighth half of a stage each), 12 walks the work for them and
