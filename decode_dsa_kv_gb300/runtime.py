@@ -615,12 +615,17 @@ def verify_drafts(drafts: torch.Tensor, target: torch.Tensor, draft: torch.Tenso
     def rows(t, name, count):
         if t.dtype != torch.float32 or t.device != dev or tuple(t.shape) != (B, count, V):
             raise ValueError(f"{name}: expected float32 {(B, count, V)} on {dev}")
-        if t.numel() and (t.stride(2) != 1 or (B > 1 and t.stride(0) != count * t.stride(1))):
-            raise ValueError(f"{name}: its rows must be evenly spaced")
-        return t.stride(1)
+        if t.numel() == 0:
+            return V
+        # (a dimension of one may have any stride)
+        step = t.stride(1) if count > 1 else t.stride(0) if B > 1 else V
+        if ((V > 1 and t.stride(2) != 1) or step < V
+                or (B > 1 and count > 1 and t.stride(0) != count * step)):
+            raise ValueError(f"{name}: its rows must be evenly spaced, V floats or more apart")
+        return step
 
     ts = rows(target, "target", n + 1)
-    ds = 0 if draft is None else rows(draft, "draft", n)
+    ds = V if draft is None else rows(draft, "draft", n)
     for t, name, dtype, shape in ((drafts, "drafts", torch.int32, (B, n)),
                                   (u, "u", torch.float32, (B, n + 1)),
                                   (n_draft, "n_draft", torch.int32, (B,)),
@@ -632,6 +637,6 @@ def verify_drafts(drafts: torch.Tensor, target: torch.Tensor, draft: torch.Tenso
     with torch.cuda.device(dev), torch.cuda.stream(st):
         tokens = torch.empty((B, n + 1), dtype=torch.int32, device=dev)
         accepted = torch.empty((B,), dtype=torch.int32, device=dev)
-        abi.check(abi.ts_verify_drafts(drafts, n_draft, target, max(ts, V), draft, max(ds, V), u,
-                                       B, n, V, tokens, accepted, err, st), "ts_verify_drafts")
+        abi.check(abi.ts_verify_drafts(drafts, n_draft, target, ts, draft, ds, u, B, n, V, tokens,
+                                       accepted, err, st), "ts_verify_drafts")
     return tokens, accepted

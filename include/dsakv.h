@@ -685,7 +685,7 @@ ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_t* cu_q, in
  *
  *   drafts   int32 [B][n]        an id outside [0, V) sets TS_DEVERR_ID_RANGE
  *                                and counts as refused
- *   n_draft  int32 [B] or NULL   in [0, n]
+ *   n_draft  int32 [B] or NULL   in [0, n] (else taken as the nearer end)
  *   target   float [B][n + 1][V] probabilities after each prefix, rows
  *                                target_stride floats apart (>= V)
  *   draft    float [B][n][V]     the draft model's, rows draft_stride apart;

@@ -137,3 +137,14 @@ def test_python_wrappers_refuse_wrong_tensors():
                 (x, p, p, u), (x, p, None, u[:, :3]), (x, p.transpose(1, 2), None, u)]:
         with pytest.raises(ValueError):
             d.verify_drafts(*bad)
+
+
+def test_verify_rows_that_lie_closer_than_their_length_are_refused():
+    import decode_dsa_kv_gb300 as d
+    drafts, u = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 2)
+    p, q = torch.full((2, 2, 5), 0.2), torch.full((2, 1, 5), 0.2)
+    row = torch.full((1, 1, 5), 0.2)
+    for target, draft in ((row.expand(2, 2, 5), q), (p, row.expand(2, 1, 5)),
+                          (p[:, :1].expand(2, 2, 5), q), (p.transpose(0, 1), q)):
+        with pytest.raises(ValueError):
+            d.verify_drafts(drafts, target, draft, u)
