@@ -2,6 +2,9 @@
 back bit for bit, chunk attention within derived bounds, draft verification
 exactly; refusals of bad data; streams, graphs and a run of all of them."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -488,6 +491,67 @@ def test_chunk_wait_that_runs_out_reports_and_recovers(d, fmt):
         c.check(*c.run())
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("H", [1000, 1024])
+def test_chunk_most_heads(d, fmt, H):
+    c = Chunk(d, fmt, 64, H, [(2, 70), (1, 300)], seed=25)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_chunk_tokens_before_the_first_request(d, fmt):
+    # cu_q starting above 0: the tokens before it are nobody's
+    c = Chunk(d, fmt, 32, 20, [(3, 200), (2, 90)], seed=26, extra=4)
+    c.check(*c.run())
+    want, want_lse = [x.clone() for x in c.run()]
+    q = torch.cat([c.q[-4:], c.q[:-4]])
+    out = torch.full_like(want, 3.0)
+    lse = torch.full_like(want_lse, 5.0)
+    c.kv.attend(q, c.cu + 4, c.table, c.ctx, True, 1 / 24, out=out, lse=lse)
+    assert c.kv.synchronize() == 0
+    assert torch.all(out[:4] == 3) and torch.all(lse[:4] == 5)
+    assert torch.equal(out[4:], want[:-4]) and torch.equal(lse[4:], want_lse[:-4])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_chunk_requests_that_share_pages(d, fmt):
+    c = Chunk(d, fmt, 64, 16, [(2, 500), (2, 500), (2, 500)], seed=27)
+    c.table[1] = c.table[0]
+    c.table[2, :4] = c.table[0, :4]
+    c.K[1] = c.K[0]
+    c.K[2] = np.concatenate([c.K[0][:256], c.K[2][256:]])
+    c.check(*c.run())
+
+
+def test_chunk_first_call_of_a_process_inside_a_capture():
+    # the launch limits and the tensor maps' encoder are set up by the first call
+    code = """
+import torch, decode_dsa_kv_gb300 as d
+for fmt in ("bf16", "e4m3"):
+    kv = d.PagedKV(4, 64, fmt)
+    kv.data.zero_()
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+    cu = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    ctx = torch.tensor([200], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 16, 576, device="cuda").bfloat16()
+    out = torch.full((2, 16, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(2, 16, device="cuda")
+    ws = kv.workspace(2, 1, 16)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kv.attend(q, cu, table, ctx, out=out, lse=lse, ws=ws)
+    g.replay()
+    assert kv.synchronize() == 0
+    assert torch.all(out == 0)
+    want = torch.log(torch.tensor([[199.0], [200.0]], device="cuda")).expand(2, 16)
+    assert torch.allclose(lse, want, rtol=0, atol=2.0 ** -18)
+print("done")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "done" in r.stdout, r.stderr
+
+
 def test_cache_past_32_bit_offsets(d):
     # slots whose byte offsets (and 16-byte offsets) pass 2^32
     rng = np.random.default_rng(14)
@@ -569,6 +633,19 @@ def test_verify_rows_with_strides_and_without_weight(d):
     for b in range(B):
         want, a = oracle.verify_drafts(x[b], n, p[b], q[b], u[b])
         assert int(accepted[b]) == a and tokens[b].tolist() == want, b
+
+
+def test_verify_rows_of_a_larger_tensor(d):
+    # one row a request, the requests further apart than the row
+    V, B = 700, 3
+    rng = np.random.default_rng(2)
+    p = distributions(rng, (B, 4), V, 1.0)
+    u = rng.random((B, 1)).astype(np.float32)
+    none = torch.empty(B, 0, dtype=torch.int32, device="cuda")
+    tokens, accepted = d.verify_drafts(none, cuda(p)[:, 1:2], None, cuda(u))
+    for b in range(B):
+        want, a = oracle.verify_drafts(np.zeros(0, np.int32), 0, p[b, 1:2], None, u[b])
+        assert int(accepted[b]) == a == 0 and tokens[b].tolist() == want
 
 
 def test_verify_reports_bad_probabilities(d):
