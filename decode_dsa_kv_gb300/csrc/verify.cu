@@ -28,7 +28,8 @@ constexpr int kThreads = 512;
 constexpr int kPer = 8;                 // tokens of a tile per thread
 constexpr int kTile = kThreads * kPer;  // 4096
 constexpr int kMaxCluster = 8;
-constexpr int kMaxV = 1 << 23;  // 256 tiles a CTA: 34 KB of sums
+constexpr int kMaxTiles = 256;  // of a CTA: 34 KB of sums
+constexpr int kMaxV = kMaxTiles * kMaxCluster * kTile;
 constexpr int kFrac = 60;
 
 // p in [0, 2) as a multiple of 2^-60 (smaller parts are cut off: below 2^-36
@@ -311,9 +312,11 @@ extern "C" ts_status ts_verify_drafts(const int32_t* drafts, const int32_t* n_dr
   if (V >= kMaxV || n > 65535 || int64_t(B) * kMaxCluster > 2147483647) return TS_ERR_UNSUPPORTED;
   const int tiles = (V + kTile - 1) / kTile;
   // As many CTAs a request as the GPU holds at once for all of them (two an
-  // SM): a second wave would wait for the first's whole chain of loads.
+  // SM): a second wave would wait for the first's whole chain of loads. But no
+  // CTA has more tiles than its shared memory has sums for.
   int cluster = 1;
-  while (cluster < kMaxCluster && cluster < tiles && int64_t(B) * cluster <= sm_count())
+  while (cluster < kMaxCluster && cluster < tiles &&
+         (int64_t(B) * cluster <= sm_count() || tiles > kMaxTiles * cluster))
     cluster *= 2;
   const int per = (tiles + cluster - 1) / cluster;
   const int smem = per * 8 * (1 + kThreads / 32);

@@ -648,6 +648,21 @@ def test_verify_rows_of_a_larger_tensor(d):
         assert int(accepted[b]) == a == 0 and tokens[b].tolist() == want
 
 
+def test_verify_large_vocabulary_for_many_requests(d):
+    # more requests than SMs, and more tiles than one block has sums for
+    B, V = 160, 1_500_001
+    target = torch.zeros(B, 1, V, device="cuda")
+    at = torch.arange(B, device="cuda") * 9001 % (V - 1)
+    rows = torch.arange(B, device="cuda")
+    target[rows, 0, at] = 0.25
+    target[rows, 0, V - 1] = 0.75
+    u = torch.where(rows % 2 == 0, 0.24, 0.26).float().view(B, 1)
+    none = torch.empty(B, 0, dtype=torch.int32, device="cuda")
+    tokens, accepted = d.verify_drafts(none, target, None, u)
+    want = torch.where(rows % 2 == 0, at, V - 1)
+    assert torch.equal(tokens[:, 0].long(), want) and torch.all(accepted == 0)
+
+
 def test_verify_reports_bad_probabilities(d):
     V = 300
     p = np.full((4, 1, V), 1 / V, dtype=np.float32)
