@@ -558,8 +558,9 @@ class PagedKV:
         """Attention of the newest tokens q [T][H][576] (request b's are rows
         cu_q[b] .. cu_q[b + 1]) over the cached positions below ctx_len[b];
         returns (out bf16 [T][H][512], lse float [T][H]). `ws`: a workspace of
-        `workspace(T, B, H)` kept by the caller; without one the call takes its
-        own from PyTorch's allocator, on its stream."""
+        `workspace(T, B, H)` kept by the caller (contiguous uint8 on the cache's
+        device); without one the call takes its own from PyTorch's allocator, on
+        its stream."""
         dev = self.data.device
         T, H = q.shape[0], q.shape[1]
         B = ctx_len.shape[0]
@@ -569,6 +570,10 @@ class PagedKV:
         if self._int32(cu_q, "cu_q", 1).shape[0] != B + 1:
             raise ValueError("cu_q: one more than the requests")
         self._table(block_table, ctx_len, B)
+        # (its size and alignment are the library's to check)
+        if ws is not None and (ws.dtype != torch.uint8 or ws.device != dev
+                               or not ws.is_contiguous()):
+            raise ValueError(f"ws: expected contiguous uint8 on {dev}")
         st = self._stream(stream, dev)
         with torch.cuda.device(dev), torch.cuda.stream(st):
             if out is None:
