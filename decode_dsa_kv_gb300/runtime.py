@@ -468,8 +468,9 @@ class PagedKV:
     8 bits (fmt "e4m3"). The caller deals out the pages; a request's position t
     lies in slot block_table[b][t // page_size] * page_size + t % page_size.
     `data` are the rows (uint8 [num_pages * page_size][row bytes]), `err` the
-    device error word. Calls enqueue on `stream` (default: the current
-    stream of the cache's device) and do not wait."""
+    device error word; making one waits until both are zero. Calls enqueue on
+    `stream` (default: the current stream of the cache's device) and do not
+    wait."""
 
     def __init__(self, num_pages: int, page_size: int = 64, fmt: str = "bf16",
                  device: str = "cuda"):
@@ -482,6 +483,12 @@ class PagedKV:
         self.data = torch.zeros((self.num_slots, abi.dsa_cache_row_bytes(self._fmt)),
                                 dtype=torch.uint8, device=dev)
         self.err = torch.zeros((1,), dtype=torch.int32, device=dev)
+        # the zeros are there before the first call, whatever its stream (inside
+        # a capture there is nothing to wait for: they are part of the graph)
+        if self.data.is_cuda:
+            with torch.cuda.device(self.data.device):
+                if not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream().synchronize()
 
     def _int32(self, t: torch.Tensor, name: str, dims: int) -> torch.Tensor:
         if t.dtype != torch.int32 or t.dim() != dims or t.device != self.data.device:
