@@ -32,9 +32,9 @@ constexpr int kMaxTiles = 256;  // of a CTA: 34 KB of sums
 constexpr int kMaxV = kMaxTiles * kMaxCluster * kTile;
 constexpr int kFrac = 60;
 
-// p in [0, 2) as a multiple of 2^-60 (smaller parts are cut off: below 2^-36
-// of a token's weight's own size only for p under 2^-36); anything else is 0
-// and sets *bad.
+// p in [0, 2) as a multiple of 2^-60 (what lies below is cut off: nothing of a
+// p of 2^-37 or more, whose last bit is at least 2^-60, and less than 2^-60 of a
+// smaller one, all of it below 2^-60); anything else is 0 and sets *bad.
 __device__ __forceinline__ uint64_t fixed(float p, int* bad) {
   const uint32_t b = __float_as_uint(p);
   if (b >= 0x40000000u) {  // 2 and more, NaN, or a sign
@@ -87,6 +87,14 @@ __device__ __forceinline__ uint64_t fixed_u(float u) {
   return sh >= 0 ? m << sh : (sh > -24 ? m >> -sh : 0);
 }
 
+// Sums of weights stop at 2^64 - 1: a row that adds up to 16 or more is told by
+// its total, whatever the order of summation.
+constexpr uint64_t kFull = ~0ull;
+__device__ __forceinline__ uint64_t add_full(uint64_t a, uint64_t b) {
+  const uint64_t s = a + b;
+  return s < a ? kFull : s;
+}
+
 struct Weights {
   const float* p;
   const float* q;  // NULL: none, or one-hot at `hot`
@@ -116,6 +124,7 @@ struct Weights {
   }
   // The warp's share of the tile's sum, in every lane; exact as long as *top
   // (the largest bits) stays below those of 2.
+  static constexpr int32_t kLargeH = (1 << 25) - (1 << 9);
   __device__ __forceinline__ uint64_t warp_tile_sum(const Tile& x, int64_t t, uint32_t* top) const {
     int32_t h = 0, l = 0, m = 0;  // |each| below kPer 2^22, the warp's below 2^30
 #pragma unroll
@@ -131,13 +140,16 @@ struct Weights {
     h = __reduce_add_sync(0xffffffffu, h);
     l = __reduce_add_sync(0xffffffffu, l);
     m = __reduce_add_sync(0xffffffffu, m);
+    // below 2^64 as long as H 2^39 is below it by more than |L| 2^17 + |M| < 2^48:
+    // else (a tile's share of some 16) value by value
+    if (h >= kLargeH) *top = ~0u;
     return (int64_t(h) << 39) + (int64_t(l) << 17) + m;
   }
 };
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  for (int d = 16; d; d >>= 1) v = add_full(v, __shfl_xor_sync(0xffffffffu, v, d));
   return v;
 }
 
@@ -196,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   int next = -1;
   for (int pass = 0; pass < 2; ++pass) {
     // every warp's part of every tile's sum; the tiles' sums follow
-    uint32_t top = 0;  // the largest bits seen: 2 and more, NaN or a sign
+    uint32_t top = 0;  // the largest bits seen: 2 and more, NaN or a sign (or a sum too large)
     Weights::Tile ahead;
     w.load(ahead, int64_t(tile0) * kTile + tid, V);
     for (int i = 0; i < tiles_per_cta; ++i) {
@@ -209,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (__syncthreads_or(top >= 0x40000000u)) {  // value by value, the bad ones left out
       for (int i = 0; i < tiles_per_cta; ++i) {
         const int64_t t0 = int64_t(tile0 + i) * kTile;
-        uint64_t v = 0;
+        uint64_t v = 0;  // (kPer values below 2: below 2^64)
         for (int j = 0; j < kPer && t0 < V; ++j)
           v += w.at(static_cast<int>(t0) + j * kThreads + tid, V, &bad);
         v = warp_sum(v);
@@ -219,13 +231,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int i = tid; i < tiles_per_cta; i += kThreads) {
       uint64_t v = 0;
-      for (int k = 0; k < kThreads / 32; ++k) v += part[i * (kThreads / 32) + k];
+      for (int k = 0; k < kThreads / 32; ++k) v = add_full(v, part[i * (kThreads / 32) + k]);
       tile_sum[i] = v;
     }
     __syncthreads();
     if (warp == 0) {
       uint64_t v = 0;
-      for (int i = lane; i < tiles_per_cta; i += 32) v += tile_sum[i];
+      for (int i = lane; i < tiles_per_cta; i += 32) v = add_full(v, tile_sum[i]);
       v = warp_sum(v);
       if (lane == 0) cta_sum = v;
     }
@@ -233,12 +245,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint64_t before = 0, total = 0;
     for (int r = 0; r < cluster; ++r) {
       const uint64_t v = ld_dsmem_u64(dsmem_addr(&cta_sum, r));
-      if (r < rank) before += v;
-      total += v;
+      if (r < rank) before += v;  // (used only where the total fits)
+      total = add_full(total, v);
     }
     const uint64_t mine = cta_sum;
     cluster_sync_all();  // every CTA has read the sums: they may change, or the CTA leave
-    if (total == 0) {    // the same in every CTA of the cluster
+    if (total == kFull) break;  // (this and the next: the same in every CTA of the cluster)
+    if (total == 0) {
       if (w.plain || (!w.q && w.hot < 0)) break;
       w.plain = true;
       continue;
@@ -279,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     break;
   }
 
-  // ---- results: the thread that holds the token, or (a row without weight)
-  // the first CTA's first thread ----
+  // ---- results: the thread that holds the token, or (a row without weight, or
+  // with too much) the first CTA's first thread ----
   if (bad) report(err, TS_DEVERR_PROB);
   if (bad_id && rank == 0) report(err, TS_DEVERR_ID_RANGE);
   if (next == -1 && (rank != 0 || tid != 0)) next = -2;

@@ -63,7 +63,7 @@ typedef enum {
 #define TS_DEVERR_TIMEOUT 0x20    /* a bounded wait inside a kernel gave up */
 #define TS_DEVERR_COUNT 0x40      /* a selection did not come out at size k */
 #define TS_DEVERR_ORDER 0x80      /* ids not strictly ascending where a call needs them so */
-#define TS_DEVERR_PROB 0x100      /* a probability that is NaN, negative or 2 or more, or a row of zeros */
+#define TS_DEVERR_PROB 0x100      /* a probability that is NaN, negative or 2 or more; a row that adds up to 0, or to 16 or more */
 
 #define TS_D 576        /* values per latent row */
 #define TS_D_LATENT 512 /* latent ("nope") part, also the V part */
@@ -694,10 +694,11 @@ ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_t* cu_q, in
  *   tokens   int32 [B][n + 1]    out: the a accepted drafts, the next token,
  *                                -1 in the places after it
  *   accepted int32 [B]           out: a
- * A row's probabilities lie in [0, 2) and add up to less than 16; one that is
- * NaN, negative or 2 or more counts as 0 and sets TS_DEVERR_PROB, and so does
- * a row without weight (its next token is -1). n >= 0, V < 2^23; B = 0
- * enqueues nothing.
+ * A row's probabilities lie in [0, 2) and add up to less than 16. One that is
+ * NaN, negative or 2 or more sets TS_DEVERR_PROB and counts as 0 in w; a draft
+ * whose p or q is one is refused. A row whose weights w are all 0, or add up to
+ * 16 or more, sets TS_DEVERR_PROB too and has -1 for its next token. n >= 0,
+ * V < 2^23; B = 0 enqueues nothing.
  * ------------------------------------------------------------------------- */
 ts_status ts_verify_drafts(const int32_t* drafts, const int32_t* n_draft, const float* target,
                            int64_t target_stride, const float* draft, int64_t draft_stride,

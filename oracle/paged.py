@@ -19,7 +19,8 @@ and out = 0, lse = -inf where no position is left.
 Verification of drafts: x_i is accepted while u_i q_i(x_i) < p_i(x_i); after a
 accepted drafts the next token is the first t whose running sum of
 w = max(p_a - q_a, 0) (p_a after the last draft, or where w vanishes) exceeds
-u_n sum w; in whole multiples of 2^-60.
+u_n sum w; in whole multiples of 2^-60. A sum of 0, or of 16 or more (2^64 - 1
+multiples), has no such t: -1.
 """
 import math
 
@@ -156,7 +157,7 @@ def verify_drafts(drafts, n_draft: int, target, draft, u):
         w = p
     total = sum(w)
     token = -1
-    if total:
+    if 0 < total < 2 ** 64 - 1:
         r = int(math.ldexp(float(u[n]), 64)) * total >> 64
         run = 0
         for t in range(V):
