@@ -529,17 +529,20 @@ class PagedKV:
     def read(self, block_table: torch.Tensor, ctx_len: torch.Tensor, pos: torch.Tensor,
              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The rows of positions pos [B][k] as bf16 [B][k][576]: sfa_mla_decode's
-        selection buffer."""
+        selection buffer. block_table int32 [B][pages a request], contiguous."""
         B, k = self._int32(pos, "pos", 2).shape
         self._table(block_table, ctx_len, B)
         if not pos.is_contiguous():
             raise ValueError("pos must be contiguous")
+        if out is not None and not self._bf16(out, "out", (B, k, D)).is_contiguous():
+            raise ValueError("out must be contiguous")
+        if B == 0 or k == 0:
+            return torch.empty((B, k, D), dtype=torch.bfloat16,
+                               device=self.data.device) if out is None else out
         st = self._stream(stream, self.data.device)
         if out is None:
             with torch.cuda.stream(st):
                 out = torch.empty((B, k, D), dtype=torch.bfloat16, device=self.data.device)
-        if not self._bf16(out, "out", (B, k, D)).is_contiguous():
-            raise ValueError("out must be contiguous")
         with torch.cuda.device(self.data.device):
             abi.check(abi.dsa_cache_read(self.data, self.num_slots, self._fmt, block_table,
                                          self._table_stride(block_table), self.page_size, pos,
@@ -564,7 +567,9 @@ class PagedKV:
                ws: torch.Tensor | None = None, stream=None):
         """Attention of the newest tokens q [T][H][576] (request b's are rows
         cu_q[b] .. cu_q[b + 1]) over the cached positions below ctx_len[b];
-        returns (out bf16 [T][H][512], lse float [T][H]). `ws`: a workspace of
+        block_table int32 [B][pages a request], contiguous. Returns (out bf16
+        [T][H][512], lse float [T][H]), fresh ones unless given; rows that no
+        request has are left as they were. `ws`: a workspace of
         `workspace(T, B, H)` kept by the caller (contiguous uint8 on the cache's
         device); without one the call takes its own from PyTorch's allocator, on
         its stream."""
@@ -581,18 +586,20 @@ class PagedKV:
         if ws is not None and (ws.dtype != torch.uint8 or ws.device != dev
                                or not ws.is_contiguous()):
             raise ValueError(f"ws: expected contiguous uint8 on {dev}")
+        if out is not None and not self._bf16(out, "out", (T, H, DV)).is_contiguous():
+            raise ValueError("out must be contiguous")
+        if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, H)
+                                or not lse.is_contiguous() or lse.device != dev):
+            raise ValueError(f"lse: expected contiguous float32 {(T, H)} on {dev}")
+        if (T == 0 or B == 0) and out is not None and lse is not None:
+            return out, lse
         st = self._stream(stream, dev)
         with torch.cuda.device(dev), torch.cuda.stream(st):
             if out is None:
                 out = torch.empty((T, H, DV), dtype=torch.bfloat16, device=dev)
             if lse is None:
                 lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-            if not self._bf16(out, "out", (T, H, DV)).is_contiguous():
-                raise ValueError("out must be contiguous")
-            if (lse.dtype != torch.float32 or tuple(lse.shape) != (T, H)
-                    or not lse.is_contiguous() or lse.device != dev):
-                raise ValueError(f"lse: expected contiguous float32 {(T, H)} on {dev}")
-            if T == 0:
+            if T == 0 or B == 0:  # no rows, or nobody's
                 return out, lse
             if ws is None:
                 ws = self.workspace(T, B, H)
