@@ -33,13 +33,12 @@
 #include <cmath>
 
 #include "cache.cuh"
+#include "chunk_plan.h"
 
 namespace dsakv {
 namespace {
 
-constexpr int kRows = 128;     // query rows of a pair's tile
-constexpr int kRowsCta = 64;   // the rows each CTA of the pair holds
-constexpr int kKeys = 256;     // keys of a tile
+constexpr int kRowsCta = 64;   // the rows of a tile that each CTA of the pair holds
 constexpr int kBlocks = 9;     // 64-wide blocks of the 576 dims
 constexpr uint32_t kQBlock = kRowsCta * 128;     // 64 rows x 64 dims
 constexpr uint32_t kQBytes = kBlocks * kQBlock;  // 72 KB, resident for a row tile
@@ -79,7 +78,6 @@ struct Layout {
 };
 constexpr int kMaxStages = 7;
 constexpr int kMaxPairs = 80;
-constexpr int kMaxCtx = 1 << 27;  // with H <= 1024, every count of the plan fits 32 bits
 constexpr uint32_t kOCol = 256;  // TMEM columns: S buffers 0..127 and 128..255, O 256..511
 constexpr uint64_t kWaitLimit = 2000000000ull;  // 2 s of global timer per wait
 constexpr uint64_t kDrainNs = 2000000ull;
@@ -151,54 +149,13 @@ struct Args {
 constexpr uint32_t kIdescNegateA = 1u << 13;
 constexpr int kStarts = 1, kEnds = 2;  // meta flags: holds the row tile's first / last keys
 
-// One request, its values brought into range.
-struct Request {
-  int q0, n, ctx;
-};
+// One request of the arguments, its values brought into range.
 __device__ __forceinline__ Request request(const Args& a, int b) {
   Request r;
   r.q0 = min(max(__ldg(a.cu_q + b), 0), a.T);
   r.n = max(min(__ldg(a.cu_q + b + 1), a.T) - r.q0, 0);
   r.ctx = min(max(__ldg(a.ctx_len + b), 0), a.max_ctx);
   return r;
-}
-__device__ __forceinline__ int row_tiles(const Args& a, const Request& r) {
-  return (r.n * a.H + kRows - 1) / kRows;  // (T H < 2^31 - 128)
-}
-// Keys that the last row of row tile j attends to.
-__device__ __forceinline__ int key_end(int H, bool causal, const Request& r, int j) {
-  if (!causal) return r.ctx;
-  // (T H < 2^31)
-  const int last = min(r.n * H - 1, j * kRows + kRows - 1);
-  return max(0, r.ctx - r.n + last / H + 1);
-}
-__device__ __forceinline__ int key_tiles(int end) { return max(1, (end + kKeys - 1) / kKeys); }
-// x / y of whole numbers >= 0, in 32 bits where they fit (64-bit division is
-// some 100 clocks of serial code).
-__device__ __noinline__ int64_t divide(int64_t x, int y) {
-  return (x >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
-}
-// Units (key tiles) of a request's first j row tiles, in closed form: row tile
-// i before the last ends with token (128 i + 127) / H, so it has
-//   1 + max(0, floor((ctx - n + (128 i + 127) / H) / 256))
-//     = 1 + max(0, floor((i + c) / 2H)),  c = floor(((ctx - n) H + 127) / 128)
-// key tiles (nested floors of quotients fold into one).
-__device__ __noinline__ int64_t units_before(int H, bool causal, const Request r, int tiles,
-                                             int j) {
-  if (!causal) return int64_t(j) * key_tiles(r.ctx);
-  int64_t s = 0;
-  const int m = min(j, tiles - 1);
-  if (m > 0) {
-    const uint32_t G = 2 * H;
-    const int c = static_cast<int>((int64_t(r.ctx - r.n) * H + kRows - 1) >> 7);
-    auto below = [&](int N) -> int64_t {  // sum of floor(i / G) over 0 <= i < N
-      const uint32_t x = max(N, 0), k = x / G;
-      return int64_t(G) * (int64_t(k) * (k - 1) / 2) + int64_t(k) * (x - k * G);
-    };
-    s = m + below(m + c) - below(c);
-  }
-  if (j == tiles) s += key_tiles(key_end(H, causal, r, tiles - 1));
-  return s;
 }
 
 // The pair's stretch of the line of all units: thread-per-request sums, then
@@ -208,7 +165,7 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
   auto units_of = [&](int b) -> int64_t {
     if (b >= a.B) return 0;
     const Request r = request(a, b);
-    return r.n ? units_before(a.H, a.causal, r, row_tiles(a, r), row_tiles(a, r)) : 0;
+    return r.n ? units_before(a.H, a.causal, r, row_tiles(a.H, r), row_tiles(a.H, r)) : 0;
   };
   // inclusive scan over the block; *all gets the sum
   auto scan = [&](int64_t v, int64_t* all) -> int64_t {
@@ -234,11 +191,8 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
 #pragma unroll 1
   for (int b = tid; b < a.B; b += threads) mine += units_of(b);
   int64_t inc = scan(mine, &total);
-  const int pairs = static_cast<int>(min(int64_t(a.pairs), total));
-  const int64_t share = pairs ? divide(total, pairs) : 0;
-  const int more = static_cast<int>(total - share * pairs);  // pairs with one unit more
-  const int64_t from = share * pair + min(pair, more);
-  const int64_t count = pair < pairs ? share + (pair < more ? 1 : 0) : 0;
+  const Stretch st = stretch_of(total, a.pairs, pair);
+  const int64_t from = st.from, count = st.count;
   if (tid == 0) bars->count = count;
   int64_t base = 0;
 #pragma unroll 1
@@ -251,18 +205,10 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
     }
     const int64_t before = base + inc - u;
     if (u && from >= before && from < before + u) {
-      const Request r = request(a, b);
-      const int tiles = row_tiles(a, r);
-      int lo = 0, hi = tiles - 1;  // the last row tile that begins at or before `from`
-#pragma unroll 1
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (units_before(a.H, a.causal, r, tiles, mid) <= from - before) lo = mid;
-        else hi = mid - 1;
-      }
+      const Place at = place_of(a.H, a.causal, request(a, b), from - before);
       bars->start_b = b;
-      bars->start_j = lo;
-      bars->start_u = static_cast<int>(from - before - units_before(a.H, a.causal, r, tiles, lo));
+      bars->start_j = at.j;
+      bars->start_u = at.u;
     }
     base += all;
   }
@@ -277,51 +223,6 @@ __device__ __forceinline__ void check_lengths(const Args& a) {
     if (c0 < 0 || c1 < c0 || c1 > a.T) report(a.err, TS_DEVERR_ORDER);
     if (ctx < 0 || ctx > a.max_ctx) report(a.err, TS_DEVERR_CTX);
   }
-}
-
-// A row tile over a range of its key tiles.
-struct Segment {
-  int b, row0;     // request; first row of the tile within the request's n x H
-  Request r;
-  int rows;        // rows of the tile
-  int t0, t1;      // key tiles
-  int end;         // keys the tile's last row attends to
-  bool starts, ends;
-};
-// Walks the segments of a pair's stretch; every role of both CTAs walks alike.
-struct Walk {
-  int b, j, u;
-  int64_t left;
-  __device__ __forceinline__ Walk(const Bars* bars)
-      : b(bars->start_b), j(bars->start_j), u(bars->start_u), left(bars->count) {}
-  __device__ __forceinline__ bool next(const Args& a, Segment& s) {
-    if (left <= 0) return false;
-    int tiles;
-    for (;; ++b, j = 0) {
-      if (b >= a.B) return false;
-      s.r = request(a, b);
-      tiles = row_tiles(a, s.r);
-      if (j < tiles) break;
-    }
-    s.b = b;
-    s.row0 = j * kRows;
-    s.rows = static_cast<int>(min(int64_t(kRows), int64_t(s.r.n) * a.H - s.row0));
-    s.end = key_end(a.H, a.causal, s.r, j);
-    const int units = key_tiles(s.end);
-    s.t0 = u;
-    s.t1 = static_cast<int>(min(int64_t(units), u + left));
-    s.starts = u == 0;
-    s.ends = s.t1 == units;
-    left -= s.t1 - s.t0;
-    if (s.ends) u = 0, ++j;
-    else u = s.t1;
-    return true;
-  }
-};
-
-// 64-key groups of key tile t that hold keys below `end`.
-__device__ __forceinline__ int groups(int end, int t) {
-  return min(4, max(0, (end - t * kKeys + 63) >> 6));
 }
 
 // 2^x on the special-function unit (relative error far below the bf16
@@ -884,7 +785,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
     return Loader{a, maps, bars, q_tile, ring, raw, rank, dsmem_addr(&bars->q_full, 0),
                   dsmem_addr(&bars->full[0], 0), lane, elect_one(), abort, k_step, min(4, k_step)};
   };
-  Walk walk(bars);
+  Walk walk{bars->start_b, bars->start_j, bars->start_u, bars->count};
   Segment sg;
   if (warp < kSoftmaxWarps) {
     // ---------------- softmax and epilogue: kParts threads per TMEM lane ----------------
