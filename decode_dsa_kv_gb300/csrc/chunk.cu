@@ -21,12 +21,15 @@
 // workspace, which chunk_merge_kernel joins in order (no atomics: results do
 // not depend on timing).
 //
-// Measured on GB300: 2048 tokens x 128 heads over 8192 bf16 positions 2.43 ms,
-// 0.88 of the measured bf16 rate (bound by the products and their issue); 32
-// single tokens x 128 heads over 32,768 positions each 280 us, 4.3 TB/s (only
-// the K stages come from HBM, and the ring does not reach over the V stages
-// between them); one token x 16 heads over 4096 positions 19 us (latency: plan,
-// first loads, softmax, epilogue, merge).
+// Measured on GB300: 2048 tokens x 128 heads over 8192 bf16 positions 2.5 to
+// 2.6 ms back to back, 0.82 to 0.86 of the measured bf16 burst rate, and 2.43 ms,
+// 0.88, as one launch behind an L2 flush, which lets the power recover (bound by
+// the products and their issue); 32 single tokens x 128 heads over 32,768
+// positions each 280 us, 4.3 TB/s (only the K stages come from HBM, and the ring
+// does not reach over the V stages between them); one token x 16 heads over 4096
+// positions 19 us (latency: plan, first loads, softmax, epilogue, merge). A row
+// tile of one key tile more costs a pair 6 us, a key tile more in the row tile it
+// has 2 to 4: a row tile is drained before the next one's scores begin.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -71,6 +74,9 @@ struct Layout {
   // such that little spills, because nearly all of the L1 is shared memory and
   // what is spilled comes back at L2's distance (bf16 rows, 88 bytes spilled by
   // the loaders at 104 registers: 2680 against 2540 us at 2048 x 128 over 8192).
+  // The kernel of bf16 rows spills nothing. That of 8-bit rows stores 120 bytes
+  // and loads 220, none of them in the converting warps (without these the count
+  // stays as it is, without the softmax's code it is zero).
   static constexpr int kSoftmaxRegs = k8 ? 200 : 176, kConvertRegs = 104, kLastRegs = k8 ? 104 : 152;
   static constexpr int kConvertThreads = kThreads - 32 * kSoftmaxWarps - 128;
   static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + kConvertThreads * kConvertRegs +
@@ -864,6 +870,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
           }
           tmem_wait_st();
         }
+        // The weights are rounded to bf16 for the value products, half a step of
+        // 2^-8 each, which is what the tensor cores' bf16 rate takes (as in the
+        // sparse decode): 2048 x 128 over 8192, the outputs' error against 64 bits
+        // goes from 0.0016 of their size, the rounding of the outputs themselves,
+        // to 0.0018. Their sum adds them unrounded, in fp32.
         const float mu = m == -INFINITY ? 0.f : m;
         uint8_t* prow = p_tile + (half * 2 + part * (kCols / 64)) * kPBlock + r * 128;
 #pragma unroll

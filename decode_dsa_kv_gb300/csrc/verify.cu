@@ -17,8 +17,9 @@
 // full-rate fp32 pipe: shifting its mantissa into 64 bits takes some 12
 // half-rate integer instructions a value instead, and was what bounded the
 // pass (128 requests x 131,072 tokens, 118 MB: 86 us; so 35 us, 0.51 of the
-// measured copy rate: the tail is each cluster's chain of sums, cluster barrier
-// and second look at one tile).
+// measured copy rate: the rest is each cluster's chain of sums, cluster barrier
+// and second look at one tile, and the pass's own instructions, 0.60 of the issue
+// slots over the launch).
 #include "common.cuh"
 
 namespace dsakv {

@@ -626,7 +626,9 @@ def verify_drafts(drafts: torch.Tensor, target: torch.Tensor, draft: torch.Tenso
                   err: torch.Tensor | None = None, stream=None):
     """ts_verify_drafts on tensors: drafts int32 [B][n], target float [B][n + 1][V],
     draft float [B][n][V] or None (certain drafts), u float [B][n + 1], n_draft
-    int32 [B] or None. Returns (tokens int32 [B][n + 1], accepted int32 [B])."""
+    int32 [B] or None. Returns (tokens int32 [B][n + 1], accepted int32 [B]).
+    `err`: a device error word (int32 [1], read with ts_read_error); without one
+    bad ids and probabilities are not reported."""
     dev = target.device
     B, n = drafts.shape
     V = target.shape[2]

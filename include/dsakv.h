@@ -566,9 +566,12 @@ ts_status dsa_group_step_host(dsa_group* g, const float* scores_h, const void* q
 /* ---------------------------------------------------------------------------
  * The paged latent cache: device rows of many requests in pages, written as
  * tokens arrive, read back by position and attended over by each request's
- * newest tokens. It serves what the host-offloaded pool does not: prefill
- * chunks, drafted tokens, layers without an indexer and contexts of at most k
- * tokens (where the selection is the whole context).
+ * newest tokens, one or many (prefill chunks, drafted tokens). The attention is
+ * dense, every token over all of its context: that of layers without an
+ * indexer, and of contexts of at most k tokens, where the selection is the
+ * whole context. Past k tokens a layer with an indexer has the sparse decode
+ * (dsa_cache_read into sfa_mla_decode, or the host-offloaded pool) for single
+ * tokens; several tokens with a selection each have no form here.
  *
  * A cache is num_slots consecutive rows (device memory, 16-byte aligned; for
  * dsa_cache_read also the device-accessible address of page-locked host
