@@ -30,3 +30,24 @@ def test_a_new_cache_is_ready_for_any_stream(fmt):
     torch.cuda.synchronize()
     assert torch.equal(kv.data, want.data)
     assert kv.synchronize() == d._abi.TS_DEVERR_SLOT_RANGE
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_cache_made_inside_a_capture(fmt):
+    # its zeros are part of the graph: every replay starts from an empty cache
+    import decode_dsa_kv_gb300 as d
+    x = torch.randn(3, 576, device="cuda").bfloat16()
+    slots = torch.tensor([5, 0, 63], dtype=torch.int32, device="cuda")
+    want = d.PagedKV(4, 16, fmt)
+    want.write(x[:, :512], x[:, 512:], slots)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kv = d.PagedKV(4, 16, fmt)
+        kv.write(x[:, :512], x[:, 512:], slots)
+    for _ in range(2):
+        kv.data.fill_(0xA5)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kv.data, want.data)
+    assert kv.synchronize() == 0
