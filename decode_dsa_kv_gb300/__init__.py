@@ -18,11 +18,13 @@ _ABI_NAMES = {
     "sfa_mla_decode_pool",
     "sfa_workspace_size", "sfa_mla_decode", "dsa_group_step", "dsa_group_step_host",
     "dsa_cache_row_bytes", "dsa_cache_write", "dsa_cache_read", "sfa_chunk_workspace_size",
-    "sfa_mla_chunk", "ts_verify_drafts", "DSA_CACHE_BF16", "DSA_CACHE_E4M3", "DsaGroup", "DsaKvError", "check", "status_string", "EXPORTS",
+    "sfa_mla_chunk", "ts_verify_drafts", "DSA_CACHE_BF16", "DSA_CACHE_E4M3",
+    "dsa_tree_plan", "dsa_cache_append", "sfa_mla_tree", "ts_verify_tree", "dsa_cache_keep",
+    "ts_beam_workspace_size", "ts_beam_select", "dsa_cache_fork", "TS_MAX_TREE", "TS_FP32", "TS_BF16", "DsaGroup", "DsaKvError", "check", "status_string", "EXPORTS",
     "LIB_PATH",
 }
 _RUNTIME_NAMES = {"HostKV", "DecodeGroup", "PinnedHost", "StepTiming", "plan_metrics", "PagedKV",
-                  "verify_drafts"}
+                  "verify_drafts", "verify_tree", "beam_select"}
 
 
 def __getattr__(name):

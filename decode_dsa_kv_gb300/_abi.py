@@ -32,6 +32,7 @@ TS_DEVERR_TIMEOUT = 0x20
 TS_DEVERR_COUNT = 0x40
 TS_DEVERR_ORDER = 0x80
 TS_DEVERR_PROB = 0x100
+TS_DEVERR_PARENT = 0x200
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -74,6 +75,16 @@ _SIGS = {
     "sfa_mla_chunk": (_I, [_P, _I64, _P, _I, _I, _I, _P, _I64, _I, _P, _I64, _I, _P, _I, _F, _P, _P,
                            _P, _SZ, _P, _P]),
     "ts_verify_drafts": (_I, [_P, _P, _P, _I64, _P, _I64, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "dsa_tree_plan": (_I, [_P, _P, _I, _I, _P, _P, _I64, _I, _I64, _P, _P, _P, _I, _P, _P]),
+    "dsa_cache_append": (_I, [_P, _I64, _P, _I64, _P, _P, _I, _P, _I, _P, _I64, _I, _P, _I64, _I64,
+                              _I, _P, _I64, _P, _P]),
+    "sfa_mla_tree": (_I, [_P, _I64, _P, _I, _I, _I, _P, _I64, _I, _P, _I64, _I, _P, _P, _I, _F, _P,
+                          _P, _P, _SZ, _P, _P]),
+    "ts_verify_tree": (_I, [_P, _P, _P, _I, _I, _P, _I64, _P, _I, _I, _P, _P, _P, _P, _P]),
+    "dsa_cache_keep": (_I, [_P, _I64, _I, _P, _I64, _I, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P]),
+    "ts_beam_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "ts_beam_select": (_I, [_P, _I, _I64, _P, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P, _P]),
+    "dsa_cache_fork": (_I, [_P, _I64, _I, _P, _I64, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
 }
 
 EXPORTS = tuple(_SIGS)
@@ -86,6 +97,9 @@ DSA_LAYOUT_SELECTION = 0
 DSA_LAYOUT_STAGED = 1
 DSA_CACHE_BF16 = 0
 DSA_CACHE_E4M3 = 1
+TS_MAX_TREE = 1024
+TS_FP32 = 0
+TS_BF16 = 1
 
 
 class DsaGroup(ctypes.Structure):
@@ -345,3 +359,60 @@ def ts_verify_drafts(drafts, n_draft, target, target_stride, draft, draft_stride
     return _lib.ts_verify_drafts(ptr(drafts), ptr(n_draft), ptr(target), target_stride, ptr(draft),
                                  draft_stride, ptr(u), B, n, V, ptr(tokens), ptr(accepted),
                                  ptr(err), stream_handle(stream))
+
+
+def dsa_tree_plan(parent, cu_q, T, B, ctx_len, block_table, table_stride, page_size, num_slots,
+                  pos, slots, mask, words, err=None, stream=None) -> int:
+    return _lib.dsa_tree_plan(ptr(parent), ptr(cu_q), T, B, ptr(ctx_len), ptr(block_table),
+                              table_stride, page_size, num_slots, ptr(pos), ptr(slots), ptr(mask),
+                              words, ptr(err), stream_handle(stream))
+
+
+def dsa_cache_append(latent, latent_stride, rope, rope_stride, pos, slots, n, freq, pairs, cache,
+                     num_slots, fmt, q_rope, q_rope_stride, q_rope_head, H, q, q_stride, err=None,
+                     stream=None) -> int:
+    return _lib.dsa_cache_append(ptr(latent), latent_stride, ptr(rope), rope_stride, ptr(pos),
+                                 ptr(slots), n, ptr(freq), int(pairs), ptr(cache), num_slots, fmt,
+                                 ptr(q_rope), q_rope_stride, q_rope_head, H, ptr(q), q_stride,
+                                 ptr(err), stream_handle(stream))
+
+
+def sfa_mla_tree(q, q_stride, cu_q, T, B, H, cache, num_slots, fmt, block_table, table_stride,
+                 page_size, ctx_len, mask, words, scale, out, lse, ws, ws_bytes, err=None,
+                 stream=None) -> int:
+    return _lib.sfa_mla_tree(ptr(q), q_stride, ptr(cu_q), T, B, H, ptr(cache), num_slots, fmt,
+                             ptr(block_table), table_stride, page_size, ptr(ctx_len), ptr(mask),
+                             words, float(scale), ptr(out), ptr(lse), ptr(ws), ws_bytes, ptr(err),
+                             stream_handle(stream))
+
+
+def ts_verify_tree(tokens, parent, cu_q, T, B, target, target_stride, u, V, depth, path, next,
+                   accepted, err=None, stream=None) -> int:
+    return _lib.ts_verify_tree(ptr(tokens), ptr(parent), ptr(cu_q), T, B, ptr(target),
+                               target_stride, ptr(u), V, depth, ptr(path), ptr(next),
+                               ptr(accepted), ptr(err), stream_handle(stream))
+
+
+def dsa_cache_keep(cache, num_slots, fmt, block_table, table_stride, page_size, cu_q, T, ctx_len, B,
+                   path, depth, accepted, new_len=None, err=None, stream=None) -> int:
+    return _lib.dsa_cache_keep(ptr(cache), num_slots, fmt, ptr(block_table), table_stride,
+                               page_size, ptr(cu_q), T, ptr(ctx_len), B, ptr(path), depth,
+                               ptr(accepted), ptr(new_len), ptr(err), stream_handle(stream))
+
+
+def ts_beam_workspace_size(B: int, K: int, V: int, n: int) -> int:
+    return int(_lib.ts_beam_workspace_size(B, K, V, n))
+
+
+def ts_beam_select(logits, dtype, row_stride, cum, B, K, V, n, tokens, parents, scores, ws,
+                   ws_bytes, err=None, stream=None) -> int:
+    return _lib.ts_beam_select(ptr(logits), dtype, row_stride, ptr(cum), B, K, V, n, ptr(tokens),
+                               ptr(parents), ptr(scores), ptr(ws), ws_bytes, ptr(err),
+                               stream_handle(stream))
+
+
+def dsa_cache_fork(cache, num_slots, fmt, block_table, table_stride, page_size, ctx_len, parents,
+                   spare, B, K, n, new_table=None, new_len=None, err=None, stream=None) -> int:
+    return _lib.dsa_cache_fork(ptr(cache), num_slots, fmt, ptr(block_table), table_stride,
+                               page_size, ptr(ctx_len), ptr(parents), ptr(spare), B, K, n,
+                               ptr(new_table), ptr(new_len), ptr(err), stream_handle(stream))

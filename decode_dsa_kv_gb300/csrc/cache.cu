@@ -12,18 +12,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// The exponent e of a group's scale 2^e: the smallest e >= -120 with
-// amax <= 448 * 2^e = 1.75 * 2^(8 + e). With amax = f * 2^a, 1 <= f < 2, that
-// is a - 8 for f <= 1.75 and a - 7 above; read off the float's bits (zero and
-// subnormals end up at the lower limit, infinity, a = 128 and f = 1, at 120).
-__device__ __forceinline__ int scale_exponent(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  const int a = static_cast<int>(b >> 23) - 127;
-  return max(a - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0), -120);
-}
-
-__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
-
 // One warp a row; lane i holds the latent values 16 i .. 16 i + 15, so a group
 // of 128 is eight lanes. One pass: a row is read once, its maxima are found in
 // the lanes that hold it, and it is written once. Bound by memory: 32,768 rows
@@ -56,30 +44,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint4 x[2] = {__ldg(src + 2 * lane), __ldg(src + 2 * lane + 1)};
   uint4 r = {};
   if (lane < 8) r = __ldg(rsrc + lane);
-  float v[16];
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(x)[i];
-    v[2 * i] = __uint_as_float(w << 16);
-    v[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-    amax = fmaxf(amax, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));  // a NaN drops out
-  }
-#pragma unroll
-  for (int d = 1; d < 8; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-  const int e = scale_exponent(amax);
-  const float inv = exp2i(-e);  // exact; so is every product below
-  uint32_t codes[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i] * inv, v[4 * i + 1] * inv),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-        make_float2(v[4 * i + 2] * inv, v[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-    codes[i] = lo | (hi << 16);
-  }
-  reinterpret_cast<uint4*>(dst)[lane] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
-  if ((lane & 7) == 0) reinterpret_cast<float*>(dst + TS_D_LATENT)[lane >> 3] = exp2i(e);
+  store_codes(dst, x, lane);
   if (lane < 8) reinterpret_cast<uint4*>(dst + kE4m3Rope)[lane] = r;
 }
 

@@ -1,5 +1,7 @@
 // sfa_mla_chunk: absorbed-MLA attention of each request's newest tokens over
-// its paged latent cache.
+// its paged latent cache; sfa_mla_tree: the same for the nodes of a drafted tree,
+// which see the cached context and, of the new positions, those that their bit
+// masks name.
 //
 // A request's n x H query rows (token-major: one latent row is every head's
 // key and value, so heads and tokens fold into one long row axis) are cut into
@@ -140,6 +142,8 @@ struct Args {
   int max_ctx;  // positions that the table has room for, at most kMaxCtx
   const int32_t* ctx_len;
   bool causal;
+  const uint32_t* tree;  // a tree's masks, [T][words]
+  int words;
   float scale_log2;  // |scale| log2(e)
   bool negate;       // scale < 0
   __nv_bfloat16* out;
@@ -228,6 +232,7 @@ __device__ __forceinline__ void check_lengths(const Args& a) {
     const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1), ctx = __ldg(a.ctx_len + b);
     if (c0 < 0 || c1 < c0 || c1 > a.T) report(a.err, TS_DEVERR_ORDER);
     if (ctx < 0 || ctx > a.max_ctx) report(a.err, TS_DEVERR_CTX);
+    if (a.tree && int64_t(c1) - c0 > 32 * a.words) report(a.err, TS_DEVERR_COUNT);
   }
 }
 
@@ -726,7 +731,17 @@ __device__ __forceinline__ void load_codes(Loader& ld, int w) {
   }
 }
 
-template <int kFmt>
+// Which of 32 new positions, number j0 and on (below 0: cached ones, all seen),
+// a node sees: bits j0 .. j0 + 31 of its mask.
+__device__ __forceinline__ uint32_t seen(const uint32_t* mask, int words, int j0) {
+  const int w = j0 >> 5;
+  auto word = [&](int i) -> uint32_t {
+    return i < 0 ? 0xffffffffu : i < words ? __ldg(mask + i) : 0u;
+  };
+  return __funnelshift_r(word(w), word(w + 1), j0 & 31);
+}
+
+template <int kFmt, bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThreads, 1)
     chunk_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   using Lay = Layout<kFmt>;
@@ -809,8 +824,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
     while (ok && walk.next(a, sg)) {
       const int rr = rank * kRowsCta + r;  // row within the tile
       int limit = 0;
+      const uint32_t* mask = nullptr;  // a tree: this row's node's
+      if (kTree && rr < sg.rows)
+        mask = a.tree + int64_t(sg.r.q0 + (sg.row0 + rr) / a.H) * a.words;
       if (rr < sg.rows)
-        limit = a.causal ? max(0, sg.r.ctx - sg.r.n + (sg.row0 + rr) / a.H + 1) : sg.r.ctx;
+        limit = a.causal && !kTree ? max(0, sg.r.ctx - sg.r.n + (sg.row0 + rr) / a.H + 1) : sg.r.ctx;
       // (the sum in parts of 64 columns, whatever the threads: both formats then
       // add in one order, and equal rows give equal results)
       float m = -INFINITY, l64[kCols / 64] = {};
@@ -831,6 +849,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
 #pragma unroll
             for (int i = 0; i < kCols; ++i)
               if (i >= nv) x[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+          }
+          if (kTree) {
+            // (only a request's last tiles hold new positions)
+            const int j0 = t * kKeys + half * 128 + part * kCols - (sg.r.ctx - sg.r.n);
+            if (j0 + kCols > 0 && mask) {
+#pragma unroll
+              for (int c = 0; c < kCols / 32; ++c) {
+                const uint32_t bits = seen(mask, a.words, j0 + 32 * c);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!(bits >> i & 1)) x[c][i] = __float_as_uint(-INFINITY);
+              }
+            }
           }
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -1204,13 +1235,13 @@ bool make_map(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_byt
 int part_rows(int T, int H) { return static_cast<int>(std::min(int64_t(T) * H, int64_t(kRows))); }
 
 // The attention's launch; the maps and the merge are the caller's.
-template <int kFmt>
+template <int kFmt, bool kTree>
 ts_status launch_chunk(const Maps& maps, const Args& a, cudaStream_t stream) {
   using Lay = Layout<kFmt>;
   static std::atomic<uint64_t> smem_set{0};
-  if (!raise_smem_limit(reinterpret_cast<const void*>(chunk_kernel<kFmt>), Lay::kSmem, smem_set))
+  if (!raise_smem_limit(reinterpret_cast<const void*>(chunk_kernel<kFmt, kTree>), Lay::kSmem, smem_set))
     return TS_ERR_CUDA;
-  chunk_kernel<kFmt><<<2 * a.pairs, Lay::kThreads, Lay::kSmem, stream>>>(maps, a);
+  chunk_kernel<kFmt, kTree><<<2 * a.pairs, Lay::kThreads, Lay::kSmem, stream>>>(maps, a);
   return launch_status();
 }
 
@@ -1225,12 +1256,15 @@ extern "C" size_t sfa_chunk_workspace_size(int T, int B, int H) {
   return align256(slots * sizeof(int4)) + align256(rows * sizeof(float2)) + rows * DSA_DV * 4;
 }
 
-extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_t* cu_q, int T,
-                                   int B, int H, const void* cache, int64_t num_slots, int fmt,
-                                   const int32_t* block_table, int64_t table_stride,
-                                   int page_size, const int32_t* ctx_len, int causal, float scale,
-                                   void* out, float* lse, void* ws, size_t ws_bytes, int32_t* err,
-                                   cudaStream_t stream) {
+namespace dsakv {
+namespace {
+
+// Both calls; a tree's masks, or NULL and causal or not.
+ts_status attend(const void* q, int64_t q_stride, const int32_t* cu_q, int T, int B, int H,
+                 const void* cache, int64_t num_slots, int fmt, const int32_t* block_table,
+                 int64_t table_stride, int page_size, const int32_t* ctx_len, bool causal,
+                 const uint32_t* tree, int words, float scale, void* out, float* lse, void* ws,
+                 size_t ws_bytes, int32_t* err, cudaStream_t stream) {
   ts_status st = cache_check(cache, num_slots, fmt);
   if (st == TS_OK) st = paging_check(block_table, table_stride, page_size, num_slots);
   if (st != TS_OK) return st;
@@ -1260,7 +1294,9 @@ extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_
   a.max_ctx = static_cast<int>(
       std::min(std::min(table_stride, int64_t(kMaxCtx)) * page_size, int64_t(kMaxCtx)));
   a.ctx_len = ctx_len;
-  a.causal = causal != 0;
+  a.causal = causal;
+  a.tree = tree;
+  a.words = words;
   // (above 0: a masked score, minus infinity, times 0 would be no number)
   a.scale_log2 = std::max(std::fabs(scale) * kLog2e, FLT_MIN);
   a.negate = scale < 0.f;
@@ -1286,14 +1322,18 @@ extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_
                     1) &&
            make_map(&maps.v, cache, num_slots, DSA_ROW_BYTES, 64, kBlocks, std::min(page_size, 64),
                     page_size >= 64 ? 2 : 1);
-    st = made ? launch_chunk<DSA_CACHE_BF16>(maps, a, stream) : TS_ERR_CUDA;
+    if (!made) return TS_ERR_CUDA;
+    st = tree ? launch_chunk<DSA_CACHE_BF16, true>(maps, a, stream)
+              : launch_chunk<DSA_CACHE_BF16, false>(maps, a, stream);
   } else {
     made = made &&
            make_map(&maps.k, a.cache + kE4m3Rope, num_slots, kE4m3RowBytes, 64, 1,
                     std::min(page_size, 64), 1) &&
            make_map(&maps.code, cache, num_slots, kE4m3RowBytes, TS_D_LATENT, 1,
                     std::min(page_size, 64), 1, true);
-    st = made ? launch_chunk<DSA_CACHE_E4M3>(maps, a, stream) : TS_ERR_CUDA;
+    if (!made) return TS_ERR_CUDA;
+    st = tree ? launch_chunk<DSA_CACHE_E4M3, true>(maps, a, stream)
+              : launch_chunk<DSA_CACHE_E4M3, false>(maps, a, stream);
   }
   if (st != TS_OK) return st;
   cudaLaunchConfig_t cfg = {};
@@ -1310,4 +1350,30 @@ extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_
     return TS_ERR_CUDA;
   }
   return TS_OK;
+}
+
+}  // namespace
+}  // namespace dsakv
+
+extern "C" ts_status sfa_mla_chunk(const void* q, int64_t q_stride, const int32_t* cu_q, int T,
+                                   int B, int H, const void* cache, int64_t num_slots, int fmt,
+                                   const int32_t* block_table, int64_t table_stride,
+                                   int page_size, const int32_t* ctx_len, int causal, float scale,
+                                   void* out, float* lse, void* ws, size_t ws_bytes, int32_t* err,
+                                   cudaStream_t stream) {
+  return attend(q, q_stride, cu_q, T, B, H, cache, num_slots, fmt, block_table, table_stride,
+                page_size, ctx_len, causal != 0, nullptr, 0, scale, out, lse, ws, ws_bytes, err,
+                stream);
+}
+
+extern "C" ts_status sfa_mla_tree(const void* q, int64_t q_stride, const int32_t* cu_q, int T,
+                                  int B, int H, const void* cache, int64_t num_slots, int fmt,
+                                  const int32_t* block_table, int64_t table_stride, int page_size,
+                                  const int32_t* ctx_len, const uint32_t* mask, int words,
+                                  float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                                  int32_t* err, cudaStream_t stream) {
+  if (words <= 0 || (T > 0 && !mask)) return TS_ERR_INVALID_ARG;
+  if (words > TS_MAX_TREE / 32) return TS_ERR_UNSUPPORTED;
+  return attend(q, q_stride, cu_q, T, B, H, cache, num_slots, fmt, block_table, table_stride,
+                page_size, ctx_len, false, mask, words, scale, out, lse, ws, ws_bytes, err, stream);
 }

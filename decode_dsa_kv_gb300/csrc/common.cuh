@@ -568,6 +568,29 @@ __device__ __forceinline__ void wait_previous_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Launches a kernel that may start setting up while the stream's previous one
+// still runs; the kernel waits for that (wait_previous_kernel) before it reads
+// or writes global memory, and what it reads may be that kernel's: plain loads
+// behind the wait, not __ldg's, which assume memory that nobody writes meanwhile.
+template <class... Params, class... Values>
+ts_status launch_after(void (*kernel)(Params...), unsigned grid, unsigned threads,
+                       cudaStream_t stream, Values... values) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, Params(values)...) != cudaSuccess) {
+    cudaGetLastError();
+    return TS_ERR_CUDA;
+  }
+  return TS_OK;
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle (sm_100 format: start,
 // leading and stride byte offsets in 16-byte units, version 1, layout 2).
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo_bytes,

@@ -61,9 +61,11 @@ typedef enum {
 #define TS_DEVERR_PTR_RANGE 0x08  /* FIFO pointer outside [0, W) */
 #define TS_DEVERR_CTX 0x10        /* ctx_len outside [k, max_ctx] */
 #define TS_DEVERR_TIMEOUT 0x20    /* a bounded wait inside a kernel gave up */
-#define TS_DEVERR_COUNT 0x40      /* a selection did not come out at size k */
+#define TS_DEVERR_COUNT 0x40      /* a selection did not come out at size k; a tree larger than its masks */
 #define TS_DEVERR_ORDER 0x80      /* ids not strictly ascending where a call needs them so */
 #define TS_DEVERR_PROB 0x100      /* a probability that is NaN, negative or 2 or more; a row that adds up to 0, or to 16 or more */
+
+#define TS_DEVERR_PARENT 0x200    /* a tree node's or a beam's parent out of range */
 
 #define TS_D 576        /* values per latent row */
 #define TS_D_LATENT 512 /* latent ("nope") part, also the V part */
@@ -707,6 +709,183 @@ ts_status ts_verify_drafts(const int32_t* drafts, const int32_t* n_draft, const 
                            int64_t target_stride, const float* draft, int64_t draft_stride,
                            const float* u, int B, int n, int V, int32_t* tokens,
                            int32_t* accepted, int32_t* err, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Several continuations of a context over the paged cache: drafted trees
+ * (dsa_tree_plan, dsa_cache_append, sfa_mla_tree, ts_verify_tree,
+ * dsa_cache_keep) and beams (ts_beam_select, dsa_cache_fork).
+ *
+ * A tree's n nodes are its request's newest tokens, in sfa_mla_chunk's packing:
+ * request b has the nodes cu_q[b] .. cu_q[b + 1] - 1 of T, and its node i is
+ * cached at the request's position ctx_len[b] - n + i (ctx_len counts them).
+ * Node i's parent is a node of a lower number of the same request, or -1: a
+ * root, which follows the cached context. A request has at most TS_MAX_TREE
+ * nodes. cu_q ascends and ctx_len[b] >= n; TS_DEVERR_ORDER and TS_DEVERR_CTX
+ * report where they do not, with the values then taken as sfa_mla_chunk's.
+ * ------------------------------------------------------------------------- */
+#define TS_MAX_TREE 1024
+
+/* dsa_tree_plan -- what the other calls need of a step's trees, once for all
+ * layers. For node i of request b, at depth e (0: a root):
+ *   pos[t]   = ctx_len[b] - n + e          its position in the text (t = cu_q[b] + i)
+ *   slots[t] = the slot of cached position ctx_len[b] - n + i, from the block table
+ *   mask[t]  = the nodes that it sees, itself and its ancestors: node j is bit
+ *              j % 32 of word j / 32
+ *   parent int32 [T]
+ *   pos, slots int32 [T], mask uint32 [T][words]  out, each may be NULL
+ * A token that no request has gets position 0, slot -1 (which dsa_cache_append
+ * skips) and an empty mask. parent NULL: chains, each node's parent the one
+ * before it. block_table may be NULL with slots. A parent that is not a lower
+ * node sets TS_DEVERR_PARENT and counts as -1; a position without a page, or
+ * with one outside the cache, sets TS_DEVERR_SLOT_RANGE and gets slot -1; more
+ * than 32 * words nodes, or more than TS_MAX_TREE, set TS_DEVERR_COUNT (masks
+ * end at their last word, nodes past TS_MAX_TREE are planned as tokens that no
+ * request has). T = 0 enqueues nothing. */
+ts_status dsa_tree_plan(const int32_t* parent, const int32_t* cu_q, int T, int B,
+                        const int32_t* ctx_len, const int32_t* block_table, int64_t table_stride,
+                        int page_size, int64_t num_slots, int32_t* pos, int32_t* slots,
+                        uint32_t* mask, int words, int32_t* err, cudaStream_t stream);
+
+/* dsa_cache_append -- dsa_cache_write with the position rotation on the way, of
+ * the rows' rope parts and of the queries'. Pair i of the 64 values (pairs != 0:
+ * 2i and 2i + 1; 0, by halves: i and i + 32) is turned by the angle
+ * pos * freq[i]:
+ *   (a, b) -> (a cos - b sin, a sin + b cos)
+ *   latent, rope, slots, n, cache   as dsa_cache_write's
+ *   pos    int32 [n]                any value
+ *   freq   double [32]              radians a position (device memory)
+ *   q_rope bf16 [n][H][64]          the queries' rope parts before the rotation,
+ *                                   tokens q_rope_stride and heads q_rope_head values apart
+ *                                   (>= 64, multiples of 8; 16-byte aligned), or NULL: no
+ *                                   queries. It may be q's own part.
+ *   q      bf16 [n][H][576]         its values 512..575 are written, tokens q_stride apart
+ *                                   (>= H * 576, a multiple of 8; 16-byte aligned)
+ * The angle is reduced exactly, whatever the position: pos times freq / 2 pi to
+ * 2^-64 of a turn. Sine and cosine are fp32, the values round once to bf16. A row whose slot
+ * is negative, or past the cache (TS_DEVERR_SLOT_RANGE), is skipped; its
+ * queries are turned all the same. n = 0 enqueues nothing. */
+ts_status dsa_cache_append(const void* latent, int64_t latent_stride, const void* rope,
+                           int64_t rope_stride, const int32_t* pos, const int32_t* slots, int n,
+                           const double* freq, int pairs, void* cache, int64_t num_slots, int fmt,
+                           const void* q_rope, int64_t q_rope_stride, int64_t q_rope_head, int H,
+                           void* q, int64_t q_stride, int32_t* err, cudaStream_t stream);
+
+/* sfa_mla_tree -- sfa_mla_chunk for the nodes of drafted trees: node i of a
+ * request sees its ctx_len - n cached positions and, of the n new ones, those
+ * that its mask names.
+ *   mask uint32 [T][words]  words in 1..TS_MAX_TREE / 32; new position j is bit
+ *                           j % 32 of word j / 32, and one past the words is not
+ *                           seen. dsa_tree_plan's, or any other; a node that
+ *                           sees nothing has out = 0 and lse = -infinity.
+ * Everything else, the workspace too, as sfa_mla_chunk. More nodes than 32 *
+ * words set TS_DEVERR_COUNT. */
+ts_status sfa_mla_tree(const void* q, int64_t q_stride, const int32_t* cu_q, int T, int B, int H,
+                       const void* cache, int64_t num_slots, int fmt, const int32_t* block_table,
+                       int64_t table_stride, int page_size, const int32_t* ctx_len,
+                       const uint32_t* mask, int words, float scale, void* out, float* lse,
+                       void* ws, size_t ws_bytes, int32_t* err, cudaStream_t stream);
+
+/* ts_verify_tree -- acceptance of a tree of drafts, such that the tokens that
+ * come out are distributed as the target's own. Node 0 of a request is its last
+ * token, accepted before; the others are drafts (chosen, as ts_beam_select
+ * chooses them, not sampled). From node x = 0 on, with the target's
+ * probabilities p after x and step s = 0, 1, ..:
+ *   t = the smallest token with p(0) + .. + p(t) > u_s * sum p, or with u NULL
+ *       the token of the largest p (ties: the lower token);
+ *   the lowest-numbered child of x whose token is t is accepted and the next x,
+ *   as long as s < depth; without one t is the next token, and the walk ends.
+ *   tokens   int32 [T]        the nodes' tokens (node 0's is not read)
+ *   parent   int32 [T]        as dsa_tree_plan's (NULL: chains)
+ *   target   float [T][V]     probabilities after each node, rows target_stride
+ *                             floats apart (>= V); with u NULL any values in
+ *                             their order (logits)
+ *   u        float [B][depth + 1]  in [0, 1), or NULL
+ *   path     int32 [B][depth + 1]  out: 0, the accepted nodes, -1 after them
+ *   next     int32 [B][depth + 1]  out: the accepted nodes' tokens, the next
+ *                                  token, -1 after it
+ *   accepted int32 [B]        out: accepted drafts, at most depth
+ * A request without a node has accepted -1 and only -1 in path and next. The
+ * sums are 64-bit multiples of 2^-60, as ts_verify_drafts'; probabilities and
+ * row sums as there: a bad value sets TS_DEVERR_PROB and counts as 0, a row
+ * that adds up to 0, or to 16 or more, sets it too and has -1 for its token.
+ * With u NULL a NaN sets TS_DEVERR_NAN and ranks lowest. 0 <= depth <=
+ * TS_MAX_TREE, V < 2^23. B = 0 enqueues nothing. */
+ts_status ts_verify_tree(const int32_t* tokens, const int32_t* parent, const int32_t* cu_q, int T,
+                         int B, const float* target, int64_t target_stride, const float* u, int V,
+                         int depth, int32_t* path, int32_t* next, int32_t* accepted, int32_t* err,
+                         cudaStream_t stream);
+
+/* dsa_cache_keep -- the rows of the accepted path moved together, one layer's
+ * cache a call: the row of node path[b][i] goes to the place of node i, for i =
+ * 1 .. accepted[b], and the request is accepted[b] + 1 positions longer than
+ * its context was:
+ *   new_len[b] = ctx_len[b] - n + accepted[b] + 1    (may be NULL, or ctx_len)
+ *   path     int32 [B][depth + 1], accepted int32 [B]  as ts_verify_tree's
+ * The rows between keep what they held. A path that does not ascend from 0
+ * within the n nodes, or an accepted outside -1..depth, sets TS_DEVERR_PARENT,
+ * a page outside the cache TS_DEVERR_SLOT_RANGE; that request's rows are then
+ * left as they were, and (a bad path) its new_len is ctx_len - n. B = 0
+ * enqueues nothing. */
+ts_status dsa_cache_keep(void* cache, int64_t num_slots, int fmt, const int32_t* block_table,
+                         int64_t table_stride, int page_size, const int32_t* cu_q, int T,
+                         const int32_t* ctx_len, int B, const int32_t* path, int depth,
+                         const int32_t* accepted, int32_t* new_len, int32_t* err,
+                         cudaStream_t stream);
+
+/* ts_beam_select -- the n best continuations of each request's K beams:
+ *   s(k, t) = cum[b][k] + logits[b][k][t] - log(sum_t' exp(logits[b][k][t']))
+ * in descending order of s, ties to the lower beam and then the lower token.
+ *   logits  dtype [B][K][V]  TS_FP32 or TS_BF16, rows row_stride values apart
+ *                            (>= V), aligned to their type
+ *   cum     float [B][K]     the beams' scores so far; -infinity: no beam
+ *   tokens, parents int32 [B][n]  out: t and k
+ *   scores  float [B][n]     out: s
+ * A continuation of score -infinity (a logit of -infinity, a beam that is none)
+ * is never chosen; where fewer than n are left, the last places have token and
+ * parent -1 and score -infinity. A finished sequence is carried on by a row
+ * that is -infinity but for its padding token. A NaN or +infinity among the
+ * logits or in cum sets TS_DEVERR_NAN and counts as -infinity. Scores are
+ * compared in 64 bits, the sums of exponentials joined in 64 bits (each
+ * exponential is fp32: the log within some 1e-7).
+ *   ws      workspace of ts_beam_workspace_size(B, K, V, n) bytes, 256-byte
+ *           aligned, contents need not be preserved; calls that may overlap on
+ *           the GPU need one each
+ * 1 <= K, 1 <= n <= 128, K * V < 2^31, B * K < 2^24. B = 0 enqueues nothing. */
+#define TS_FP32 0
+#define TS_BF16 1
+size_t ts_beam_workspace_size(int B, int K, int V, int n);
+ts_status ts_beam_select(const void* logits, int dtype, int64_t row_stride, const float* cum,
+                         int B, int K, int V, int n, int32_t* tokens, int32_t* parents,
+                         float* scores, void* ws, size_t ws_bytes, int32_t* err,
+                         cudaStream_t stream);
+
+/* dsa_cache_fork -- the sequences' states reordered after ts_beam_select: new
+ * sequence i = b * n + j of B * n continues old sequence b * K + parents[i] of
+ * B * K. The old one's full pages are shared; the page that its next row goes
+ * to is spare[i], with the rows of its partial last page copied there:
+ *   w = ctx_len of the parent / page_size
+ *   new_table[i] = the parent's entries 0 .. w - 1, spare[i], -1 ..
+ *   new_len[i]   = the parent's ctx_len
+ *   block_table int32 [B * K][table_stride], ctx_len int32 [B * K]
+ *   parents     int32 [B][n]         in 0..K-1; -1: new sequence i is none
+ *                                    (length 0, its table row all -1)
+ *   spare       int32 [B * n]        pages of the cache, each named once and held
+ *                                    by no old sequence (or equal to the
+ *                                    parent's own last page, if no other new
+ *                                    sequence has that parent: nothing is
+ *                                    copied then)
+ *   new_table   int32 [B * n][table_stride], new_len int32 [B * n]  out, other
+ *               memory than the inputs'; both NULL: the rows alone, for the
+ *               other layers' caches
+ * A parent out of range sets TS_DEVERR_PARENT and counts as -1; a page outside
+ * the cache sets TS_DEVERR_SLOT_RANGE, its rows are then not copied; a ctx_len
+ * below 0 or past the table sets TS_DEVERR_CTX (taken as the nearest valid
+ * value). A sequence that fills its table gets no spare page. B = 0 enqueues
+ * nothing. */
+ts_status dsa_cache_fork(void* cache, int64_t num_slots, int fmt, const int32_t* block_table,
+                         int64_t table_stride, int page_size, const int32_t* ctx_len,
+                         const int32_t* parents, const int32_t* spare, int B, int K, int n,
+                         int32_t* new_table, int32_t* new_len, int32_t* err, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
