@@ -1,24 +1,25 @@
 // ts_beam_select: the n best of a request's K x V continuations, and
 // dsa_cache_fork: the sequences' block tables and last pages in their new order.
 //
-// Two kernels. beam_rows_kernel reads the logits, once: a CTA takes a piece of
-// one beam's row into registers and leaves the piece's n best and its sum of
-// exponentials. beam_merge_kernel, a CTA a request, joins the sums and takes
-// the n best of the pieces' best. What bounds them is the one read of the
-// logits and, with 16-bit ones, the instructions for each value.
+// Two kernels. beam_rows_kernel reads the logits: a CTA streams a piece of one
+// beam's row and leaves the piece's n best and its sums of exponentials.
+// beam_merge_kernel, a CTA a request, joins the sums and takes the n best of the
+// pieces' best.
 //
 // The n best of many values without sorting them: cut the values into groups,
 // at least n of them; the n-th largest of the groups' maxima is a bound that at
 // least n values reach and, unless the large values sit in few groups, not many
-// more. Those few are listed in shared memory, and a value's place is the number
+// more. While a row streams by, a thread keeps only the maximum of each 64 bytes
+// it reads; with the bound it reads again the few that reach it. The values
+// above the bound are listed in shared memory, and a value's place is the number
 // of larger ones. Where more reach the bound than the list holds (rows of equal
 // values, or sorted ones), the bound is raised by bisection until they fit.
 //
-// A sum of exponentials is s e^m. For a piece m is E log 2 with E whole, and
-// exp(x - m) is taken as 2^(x log2(e) - E) with log2(e) in two floats: pieces then
+// A sum of exponentials is s e^m. For a warp m is E log 2 with E whole, and
+// exp(x - m) is taken as 2^(x log2(e) - E) with log2(e) in two floats: sums then
 // join exactly, by powers of two, and no rounding of a maximum, which the whole
-// row would share, enters the result. (Where a piece's largest value is past
-// 2^20 in size, rows of a type's lowest value, m is that value itself.)
+// row would share, enters the result. (Where a warp's largest value is past 2^20
+// in size, rows of a type's lowest value, m is that value itself.)
 #include <algorithm>
 #include <climits>
 
@@ -27,9 +28,11 @@
 namespace dsakv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxN = 128;
+constexpr int kMaxN = 64;
+constexpr int kMaxRounds = 8;
+constexpr int kStages = 3;  // rounds of a piece on their way or in use
 constexpr int kList = 512;
 constexpr float kLog2eHi = 1.44269502162933349609f, kLog2eLo = 1.92596299112661746887e-8f;
 
@@ -62,7 +65,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
 __device__ __forceinline__ uint64_t key_of(float x, int t) {
   return uint64_t(in_order(x)) << 32 | (0xffffffffu - static_cast<uint32_t>(t));
 }
-constexpr uint32_t kNoValue = 0x007fffffu;  // in_order(-infinity): never a candidate
 
 struct Piece {
   float s;    // sum of exp(x - m)
@@ -74,189 +76,344 @@ constexpr int kWide = INT_MAX;
 constexpr double kLn2 = 0.693147180559945309417;
 __device__ __forceinline__ double Piece::m() const { return e == kWide ? double(top) : e * kLn2; }
 
+// Packed pairs of fp32 values.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+
+// Word i of four that hold 16 bytes of a row.
+__device__ __forceinline__ uint32_t& word(uint4& q, int i) {
+  return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+}
+__device__ __forceinline__ uint32_t word(const uint4& q, int i) {
+  return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+}
+
+// 16 bytes of a row, kept as they came; a round of them.
+constexpr int kQuads = 4;
 template <class T>
-struct Quad;  // 16 bytes of a row
+struct Quad;
 template <>
 struct Quad<float> {
   static constexpr int kValues = 4;
-  static __device__ __forceinline__ void widen(const uint4& q, float* x) {
-    x[0] = __uint_as_float(q.x);
-    x[1] = __uint_as_float(q.y);
-    x[2] = __uint_as_float(q.z);
-    x[3] = __uint_as_float(q.w);
+  static constexpr uint32_t kNone = 0xff800000u;  // a word of -infinity
+  static __device__ __forceinline__ float value(const uint4& q, int c) {
+    return __uint_as_float(word(q, c));
   }
-  static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
+  static __device__ __forceinline__ void set(uint4& q, int c, float x) {
+    word(q, c) = __float_as_uint(x);
+  }
+  static __device__ __forceinline__ float load(const float* p) { return __ldg(p); }
+  static __device__ __forceinline__ float top(const uint4 (&x)[kQuads]) {
+    float m[kQuads];
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i)
+      m[i] = fmaxf(fmaxf(value(x[i], 0), value(x[i], 1)), fmaxf(value(x[i], 2), value(x[i], 3)));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  }
 };
 template <>
 struct Quad<__nv_bfloat16> {
   static constexpr int kValues = 8;
-  static __device__ __forceinline__ void widen(const uint4& q, float* x) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  static constexpr uint32_t kNone = 0xff80ff80u;
+  static __device__ __forceinline__ float value(const uint4& q, int c) {
+    const uint32_t w = word(q, c >> 1);
+    return __uint_as_float(c & 1 ? w & 0xffff0000u : w << 16);
   }
-  static __device__ __forceinline__ float one(const __nv_bfloat16* p) {
+  static __device__ __forceinline__ void set(uint4& q, int c, float x) {
+    uint32_t& w = word(q, c >> 1);
+    const uint32_t b = __float_as_uint(x);
+    w = c & 1 ? (w & 0xffffu) | (b & 0xffff0000u) : (w & 0xffff0000u) | b >> 16;
+  }
+  static __device__ __forceinline__ float load(const __nv_bfloat16* p) {
     return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const unsigned short*>(p))) << 16);
+  }
+  static __device__ __forceinline__ float top(const uint4 (&x)[kQuads]) {
+    auto as2 = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    __nv_bfloat162 m[kQuads];
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i)
+      m[i] = __hmax2(__hmax2(as2(x[i].x), as2(x[i].y)), __hmax2(as2(x[i].z), as2(x[i].w)));
+    const __nv_bfloat162 all = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+    return fmaxf(__low2float(all), __high2float(all));
   }
 };
 
 // Threads whose maximum is a group's: as many groups as a power of two from 4 n
-// on, if there are threads for it.
+// on, or (n above 32) from 2 n on.
 __host__ __device__ inline int group_threads(int n) {
-  return n <= 8 ? 8 : n <= 16 ? 4 : n <= 32 ? 2 : 1;
+  return n <= 8 ? 4 : n <= 16 ? 2 : 1;
 }
 
 // The n-th largest of the first `groups` words of `of` (all different, or equal
 // ones in the order of their places), found by thread i < groups for word i.
+// (a power of two from 32 on; 16-byte aligned)
 __device__ __forceinline__ bool is_nth(const uint32_t* of, int groups, int i, int n) {
   const uint32_t v = of[i];
   int above = 0;
-  for (int j = 0; j < groups; ++j) above += of[j] > v || (of[j] == v && j < i);
+#pragma unroll 2
+  for (int j = 0; j < groups; j += 4) {
+    const uint4 o = *reinterpret_cast<const uint4*>(of + j);
+    above += (o.x > v || (o.x == v && j < i)) + (o.y > v || (o.y == v && j + 1 < i)) +
+             (o.z > v || (o.z == v && j + 2 < i)) + (o.w > v || (o.w == v && j + 3 < i));
+  }
   return above == n - 1;
 }
 
-// kQuads 16-byte loads a thread.
-template <class T, int kQuads>
-__global__ void __launch_bounds__(kThreads)
+// A piece is `rounds` rounds of kQuads 16-byte loads a thread. They go through
+// shared memory, each thread's through places of its own, so that the next two
+// rounds are on their way without a register (in registers, one round ahead, the
+// compiler spilled: 64 against 58 us for the version that read no ahead).
+template <class T>
+__global__ void __launch_bounds__(kThreads, 7)
     beam_rows_kernel(const T* __restrict__ logits, int64_t row_stride, int V, int n, int pieces,
-                     uint64_t* __restrict__ best, Piece* __restrict__ sums, int32_t* err) {
-  constexpr int kValues = Quad<T>::kValues, kEach = kQuads * kValues;
-  __shared__ uint32_t maxima[kThreads];
-  __shared__ uint64_t list[kList];
-  __shared__ uint64_t bound;
-  __shared__ int listed;
-  __shared__ uint32_t warp_top[kWarps];
-  __shared__ float warp_sum[kWarps];
+                     int rounds, uint64_t* __restrict__ best, Piece* __restrict__ sums,
+                     int32_t* err) {
+  using Q = Quad<T>;
+  constexpr int kValues = Q::kValues;
+  constexpr int kStep = kThreads * kValues;   // tokens between a thread's loads
+  constexpr int kRound = kStep * kQuads;      // tokens of a round
+  __shared__ __align__(16) uint32_t maxima[kThreads];
+  __shared__ uint32_t bound, most;
+  __shared__ int listed, hit;
+  extern __shared__ __align__(16) uint4 ring[];  // [kStages][kQuads][kThreads]
+  float* round_top = reinterpret_cast<float*>(ring + kStages * kQuads * kThreads);  // [rounds][kThreads]
+  // once the rounds are through: the values above the bound, and where they are
+  uint64_t* list = reinterpret_cast<uint64_t*>(ring);
+  uint32_t* hits = reinterpret_cast<uint32_t*>(list + kList);
+  static_assert(kList * 8 + kMaxRounds * kThreads * 4 <= kStages * kQuads * kThreads * 16, "lists");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / pieces;
-  const int piece = blockIdx.x % pieces;
+  const int piece = blockIdx.x - static_cast<int>(row) * pieces;
   const T* p = logits + row * row_stride;
   // the row from the 16-byte boundary at or below its first value on
   const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
-  const int t0 = (piece * kThreads * kQuads + tid) * kValues - shift;  // of this thread's first load
-  constexpr int kStep = kThreads * kValues;                            // tokens between its loads
-  float x[kEach];
-  uint4 raw[kQuads];
-#pragma unroll
-  for (int i = 0; i < kQuads; ++i) {
-    const int t = t0 + i * kStep;
-    if (t >= 0 && t + kValues <= V) raw[i] = __ldcs(reinterpret_cast<const uint4*>(p + t));
-  }
-#pragma unroll
-  for (int i = 0; i < kQuads; ++i) {
-    const int t = t0 + i * kStep;
+  const int from = piece * rounds * kRound - shift;  // the piece's first token
+  const int t0 = from + tid * kValues;               // of this thread's first load
+  // the row's ends: whole loads where they lie inside, else value by value
+  auto load_end = [&](uint4& x, int t) {
+    x = make_uint4(Q::kNone, Q::kNone, Q::kNone, Q::kNone);
     if (t >= 0 && t + kValues <= V) {
-      Quad<T>::widen(raw[i], x + i * kValues);
-    } else {
+      x = __ldcs(reinterpret_cast<const uint4*>(p + t));
+    } else if (t < V && t + kValues > 0) {
 #pragma unroll
       for (int c = 0; c < kValues; ++c)
-        x[i * kValues + c] = t + c >= 0 && t + c < V ? Quad<T>::one(p + t + c) : -INFINITY;
-    }
-  }
-  if (tid == 0) listed = 0;
-  // NaN and +infinity count as -infinity. (A maximum passes NaNs over; they show
-  // in the sum.)
-  float mx = -INFINITY;
-  auto take_out = [&]() {
-    report(err, TS_DEVERR_NAN);
-    mx = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      if (!(x[j] < INFINITY)) x[j] = -INFINITY;
-      mx = fmaxf(mx, x[j]);
+        if (t + c >= 0 && t + c < V) Q::set(x, c, Q::load(p + t + c));
     }
   };
+  auto send = [&](int r) {
+    if (r < rounds) {
+      uint4* to = ring + (r % kStages) * (kQuads * kThreads) + tid;
+      const int at = from + r * kRound, t = t0 + r * kRound;
+      if (at >= 0 && at + kRound <= V) {
 #pragma unroll
-  for (int j = 0; j < kEach; ++j) mx = fmaxf(mx, x[j]);
-  if (mx == INFINITY) take_out();
-  // the groups' maxima
-  const int per = group_threads(n), groups = kThreads / per;
-  {
-    uint32_t m = in_order(mx);
-    for (int d = 1; d < per; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (tid % per == 0) maxima[tid / per] = m;
-    m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0) warp_top[warp] = m;
-  }
-  __syncthreads();
-  if (tid < groups && is_nth(maxima, groups, tid, n)) bound = uint64_t(maxima[tid]) << 32;
-  uint32_t most = warp_top[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) most = max(most, warp_top[w]);
-  const float top = from_order(most);
-  const bool wide = fabsf(top) > 0x1p20f && top > -INFINITY;
-  const float e = wide || top == -INFINITY ? 0.f : ceilf(top * kLog2eHi);
-  auto sum = [&]() -> float {
-    float s[4] = {};
-    if (!wide) {
-#pragma unroll
-      for (int j = 0; j < kEach; ++j)
-        s[j & 3] += fast_exp2(fmaf(x[j], kLog2eLo, fmaf(x[j], kLog2eHi, -e)));
-    } else {
-      for (int j = 0; j < kEach; ++j) s[j & 3] += fast_exp2((x[j] - top) * kLog2eHi);
-    }
-    float all = (s[0] + s[1]) + (s[2] + s[3]);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
-    return all;
-  };
-  float all = sum();
-  if (!(all < INFINITY)) {  // (the whole warp)
-    take_out();
-    all = sum();
-  }
-  if (lane == 0) warp_sum[warp] = all;
-  __syncthreads();
-  launch_dependents();
-  if (tid == 0) {
-    float s = warp_sum[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) s += warp_sum[w];
-    sums[blockIdx.x] = {top == -INFINITY ? 0.f : s, wide ? kWide : static_cast<int>(e), top};
-  }
-  auto add_above = [&](uint64_t least) {
-    if (uint64_t(in_order(mx)) << 32 < (least & ~0xffffffffull)) return;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const uint64_t k = key_of(x[j], t0 + (j / kValues) * kStep + j % kValues);
-      if (k >= least && (k >> 32) > kNoValue) {
-        const int at = atomicAdd(&listed, 1);
-        if (at < kList) list[at] = k;
+        for (int i = 0; i < kQuads; ++i)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           smem_addr(to + i * kThreads)),
+                       "l"(p + (t + i * kStep))
+                       : "memory");
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kQuads; ++i) load_end(to[i * kThreads], t + i * kStep);
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  uint64_t least = bound;
-  add_above(least);
+  if (tid == 0) {
+    listed = hit = 0;
+    most = 0;
+  }
+
+  // ---- the stream ----
+  float mine = -INFINITY;  // this thread's maximum
+  // the warp's reference: E, or (wide) its maximum, or nothing yet; a value past
+  // `limit` needs another one
+  float e = 0.f, ref = -INFINITY, limit = -INFINITY;
+  bool wide = false;
+  uint64_t sum[2] = {};
+  auto add = [&](const uint4 (&x)[kQuads]) {
+    if (wide) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+        for (int c = 0; c < kValues; ++c) s += fast_exp2((Q::value(x[i], c) - ref) * kLog2eHi);
+      sum[0] = add2(sum[0], pair(s, 0.f));
+      return;
+    }
+    const uint64_t hi = pair(kLog2eHi, kLog2eHi), lo = pair(kLog2eLo, kLog2eLo),
+                   minus_e = pair(-e, -e);
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+      for (int c = 0; c < kValues; c += 2) {
+        const uint64_t v = pair(Q::value(x[i], c), Q::value(x[i], c + 1));
+        const float2 y = unpair(fma2(v, lo, fma2(v, hi, minus_e)));
+        sum[c >> 1 & 1] = add2(sum[c >> 1 & 1], pair(fast_exp2(y.x), fast_exp2(y.y)));
+      }
+  };
+  // NaN and +infinity count as -infinity. (A maximum passes NaNs over; they show
+  // in the sums.)
+  auto take_out = [&](uint4 (&x)[kQuads]) {
+    report(err, TS_DEVERR_NAN);
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+      for (int c = 0; c < kValues; ++c)
+        if (!(Q::value(x[i], c) < INFINITY)) Q::set(x[i], c, -INFINITY);
+  };
+  auto round = [&](uint4 (&x)[kQuads], int r) {
+    float top = Q::top(x);
+    if (__any_sync(0xffffffffu, !(top <= limit))) {
+      // (the first round, a much larger value, NaNs alone or an infinity)
+      if (!(top < INFINITY)) {
+        take_out(x);
+        top = Q::top(x);
+      }
+      const float all = from_order(__reduce_max_sync(0xffffffffu, in_order(fmaxf(top, mine))));
+      if (!(all <= limit)) {
+        const bool was_wide = wide, none = limit == -INFINITY;
+        const float was_e = e, was_ref = ref;
+        wide = fabsf(all) > 0x1p20f;
+        ref = all;
+        e = wide ? 0.f : ceilf(all * kLog2eHi);
+        limit = wide ? all : (e + 64.f) * static_cast<float>(kLn2);
+        float f = 0.f;
+        if (!none && !was_wide && !wide) f = ldexpf(1.f, max(static_cast<int>(was_e - e), -200));
+        else if (!none)
+          f = static_cast<float>(exp((was_wide ? double(was_ref) : was_e * kLn2) -
+                                     (wide ? double(ref) : e * kLn2)));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 y = unpair(sum[k]);
+          sum[k] = pair(y.x * f, y.y * f);
+        }
+      }
+    }
+    const uint64_t before[2] = {sum[0], sum[1]};
+    add(x);
+    {
+      const float2 y = unpair(add2(sum[0], sum[1]));
+      if (__any_sync(0xffffffffu, !(y.x + y.y < INFINITY))) {
+        take_out(x);
+        sum[0] = before[0];
+        sum[1] = before[1];
+        add(x);
+      }
+    }
+    round_top[r * kThreads + tid] = top;
+    mine = fmaxf(mine, top);
+  };
+  {
+#pragma unroll
+    for (int r = 0; r < kStages - 1; ++r) send(r);
+#pragma unroll 1
+    for (int r = 0; r < rounds; ++r) {
+      send(r + kStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      uint4 x[kQuads];
+      const uint4* at = ring + (r % kStages) * (kQuads * kThreads) + tid;
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) x[i] = at[i * kThreads];
+      round(x, r);
+    }
+  }
+  launch_dependents();
+  {
+    const float2 y = unpair(add2(sum[0], sum[1]));
+    float s = y.x + y.y;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane == 0)
+      sums[int64_t(blockIdx.x) * kWarps + warp] = {s, wide ? kWide : static_cast<int>(e), ref};
+  }
+
+  // ---- the n best ----
+  const int per = group_threads(n), groups = kThreads / per;
+  {
+    uint32_t m = in_order(mine);
+    for (int d = 1; d < per; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (tid % per == 0) maxima[tid / per] = m;
+  }
+  __syncthreads();
+  if (tid < groups) {
+    if (is_nth(maxima, groups, tid, n)) bound = maxima[tid];
+    atomicMax(&most, maxima[tid]);
+  }
+  __syncthreads();
+  auto put = [&](uint64_t k) {
+    const int at = atomicAdd(&listed, 1);
+    if (at < kList) list[at] = k;
+  };
+  const float least = from_order(bound);
+  // the threads' rounds that reach it, then all of their loads at once
+  if (mine >= least)
+#pragma unroll 4
+    for (int r = 0; r < rounds; ++r)
+      if (round_top[r * kThreads + tid] >= least) hits[atomicAdd(&hit, 1)] = r * kThreads + tid;
+  __syncthreads();
+#pragma unroll 1
+  for (int j = tid; j < hit * kQuads; j += kThreads) {
+    const int at = hits[j / kQuads], r = at / kThreads, i = j % kQuads;
+    const int t = from + r * kRound + i * kStep + (at % kThreads) * kValues;
+    uint4 x;
+    load_end(x, t);
+#pragma unroll
+    for (int c = 0; c < kValues; ++c) {
+      const float v = Q::value(x, c);
+      if (v >= least && v > -INFINITY && v < INFINITY) put(key_of(v, t + c));
+    }
+  }
   __syncthreads();
   if (listed > kList) {
     // raised until at least n and at most kList keys (all different) reach it
-    uint64_t lo = least, hi = ~0ull;  // n or more reach lo, none hi
+    auto keys = [&](auto&& f) {
+#pragma unroll 1
+      for (int t = max(from, 0) + tid; t < min(from + rounds * kRound, V); t += kThreads) {
+        const float v = Q::load(p + t);
+        if (v > -INFINITY && v < INFINITY) f(key_of(v, t));
+      }
+    };
+    // n or more reach lo, none hi
+    uint64_t lo = uint64_t(bound) << 32, hi = (uint64_t(most) << 32) + (uint64_t(1) << 32);
     for (;;) {
       const uint64_t mid = lo + (hi - lo) / 2;
-      int mine = 0;
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) {
-        const uint64_t k = key_of(x[j], t0 + (j / kValues) * kStep + j % kValues);
-        mine += k >= mid && (k >> 32) > kNoValue;
-      }
+      int reach = 0;
+      keys([&](uint64_t k) { reach += k >= mid; });
       __syncthreads();
       if (tid == 0) listed = 0;
       __syncthreads();
-      mine = __reduce_add_sync(0xffffffffu, mine);
-      if (lane == 0) atomicAdd(&listed, mine);
+      reach = __reduce_add_sync(0xffffffffu, reach);
+      if (lane == 0) atomicAdd(&listed, reach);
       __syncthreads();
-      const int all = listed;
-      if (all >= n) lo = mid;
+      reach = listed;
+      if (reach >= n) lo = mid;
       else hi = mid;
-      if ((all >= n && all <= kList) || hi - lo <= 1) break;
+      if ((reach >= n && reach <= kList) || hi - lo <= 1) break;
     }
     __syncthreads();
     if (tid == 0) listed = 0;
     __syncthreads();
-    add_above(lo);
+    keys([&](uint64_t k) {
+      if (k >= lo) put(k);
+    });
     __syncthreads();
   }
   const int count = min(listed, kList);
@@ -284,71 +441,95 @@ struct Beam {
   double m, rest;
 };
 
+// One CTA a request. Its time is its chain: the pieces' sums and best, which are
+// all on their way from the start, a logarithm for each beam (fp64, all beams at
+// once), and three barriers.
+constexpr int kAhead = 4;  // candidates a thread holds in registers
 __global__ void __launch_bounds__(kThreads)
     beam_merge_kernel(const uint64_t* best, const Piece* sums, const float* cum, int K, int V,
                       int n, int pieces, Beam* beams, int32_t* tokens, int32_t* parents,
                       float* scores, int32_t* err) {
   __shared__ uint64_t score[kList];
   __shared__ uint32_t place[kList];
-  __shared__ float maxima[kThreads];
-  __shared__ float bound;
+  __shared__ __align__(16) uint32_t maxima[kThreads];
+  __shared__ uint32_t bound;
   __shared__ int listed;
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   launch_dependents();
   wait_previous_kernel();
-  if (tid == 0) {
-    listed = 0;
-    bound = -INFINITY;
+  // candidates lie in the order of (beam, piece, place there)
+  const uint32_t each = pieces * n, all = K * each;
+  best += int64_t(b) * all;
+  uint64_t ahead[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const uint32_t i = tid + j * kThreads;
+    ahead[j] = i < all ? best[i] : 0;
   }
-  // every beam's sum of exponentials; a warp a beam
+  if (tid == 0) listed = 0;
+  // every beam's sum of exponentials, in whole multiples of 2^-30 of 2^e: a warp
+  // a beam
   beams += int64_t(b) * K;
   for (int k = warp; k < K; k += kWarps) {
-    const Piece* of = sums + (int64_t(b) * K + k) * pieces;
-    double m = -INFINITY;
+    const int parts = pieces * kWarps;
+    const Piece* of = sums + (int64_t(b) * K + k) * parts;
+    Piece first = {0.f, 0, 0.f};
+    if (lane < parts) first = of[lane];
+    const float c = cum[int64_t(b) * K + k];
+    auto piece = [&](int i) { return i == lane ? first : of[i]; };
     int e = INT_MIN;  // of the pieces that are not wide
-    for (int i = lane; i < pieces; i += 32) {
-      const Piece p = of[i];
-      if (p.s > 0.f) m = fmax(m, p.m());
+    uint32_t top = 0; // of those that are
+    for (int i = lane; i < parts; i += 32) {
+      const Piece p = piece(i);
       if (p.s > 0.f && p.e != kWide) e = max(e, p.e);
+      if (p.s > 0.f && p.e == kWide) top = max(top, in_order(p.top));
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, d));
     e = __reduce_max_sync(0xffffffffu, e);
-    const bool whole = e != INT_MIN && m == e * kLn2;  // m is a power of two's
+    top = __reduce_max_sync(0xffffffffu, top);
+    Beam beam = {e * kLn2, 0};
     double s = 0;
-    for (int i = lane; i < pieces; i += 32) {
-      const Piece p = of[i];
-      if (!(p.s > 0.f)) continue;
-      if (whole && p.e != kWide) s += double(ldexpf(p.s, max(p.e - e, -200)));
-      else s += p.s * exp(p.m() - m);
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (lane == 0) {
-      float c = cum[int64_t(b) * K + k];
-      if (!(c < INFINITY)) {
-        report(err, TS_DEVERR_NAN);
-        c = -INFINITY;
+    if (top == 0 || (e != INT_MIN && from_order(top) < 0.f)) {
+      // (a wide piece below the others adds nothing)
+      uint64_t whole = 0;
+      for (int i = lane; i < parts; i += 32) {
+        const Piece p = piece(i);
+        if (p.s > 0.f && p.e != kWide)
+          whole += __float2ull_rn(ldexpf(p.s, max(p.e - e, -100) + 30));
       }
-      beams[k] = {m, s > 0 && c > -INFINITY ? double(c) - log(s) : -INFINITY};
+#pragma unroll
+      for (int d = 16; d; d >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, d);
+      s = static_cast<double>(whole) * 0x1p-30;
+    } else {
+      beam.m = from_order(top);
+      for (int i = lane; i < parts; i += 32) {
+        const Piece p = piece(i);
+        if (p.s > 0.f) s += p.s * exp(p.m() - beam.m);
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    }
+    if (lane == 0) {
+      if (!(c < INFINITY)) report(err, TS_DEVERR_NAN);
+      beam.rest = c < INFINITY && c > -INFINITY ? s : 0;
+      beams[k] = beam;
     }
   }
   __syncthreads();
-  // Warps take beams, or (few beams) equal slices of them; candidates lie in
-  // order of (beam, piece, place there).
-  const int slices = K < kWarps ? kWarps / K : 1;
-  const int each = pieces * n, slice = (each + slices - 1) / slices;
-  best += int64_t(b) * K * each;
+  for (int k = tid; k < K; k += kThreads) {
+    const double s = beams[k].rest;
+    beams[k].rest = s > 0 ? double(cum[int64_t(b) * K + k]) - log(s) : -INFINITY;
+  }
+  __syncthreads();
   auto walk = [&](auto&& f) {
-    for (int u = warp; u < K * slices; u += kWarps) {
-      const int k = u / slices, from = (u - k * slices) * slice, to = min(each, from + slice);
+    auto one = [&](uint32_t i, uint64_t key) {
+      const int k = i / each;
       const Beam beam = beams[k];
-      if (beam.rest == -INFINITY) continue;
-      for (int i = from + lane; i < to; i += 32) {
-        const uint64_t key = best[int64_t(k) * each + i];
-        if (key) f(k, beam, key);
-      }
-    }
+      if (key && beam.rest > -INFINITY) f(k, beam, key);
+    };
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (ahead[j]) one(tid + j * kThreads, ahead[j]);
+    for (uint32_t i = tid + kAhead * kThreads; i < all; i += kThreads) one(i, best[i]);
   };
   auto candidate = [&](int k, const Beam& beam, uint64_t key) -> Candidate {
     const double x = from_order(static_cast<uint32_t>(key >> 32));
@@ -375,16 +556,11 @@ __global__ void __launch_bounds__(kThreads)
   const int per = group_threads(n), groups = kThreads / per;
   for (int d = 1; d < per; d <<= 1)
     mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, d));
-  if (tid % per == 0) maxima[tid / per] = mine;
+  if (tid % per == 0) maxima[tid / per] = in_order(mine);
   __syncthreads();
-  if (tid < groups) {
-    const float v = maxima[tid];
-    int above = 0;
-    for (int j = 0; j < groups; ++j) above += maxima[j] > v || (maxima[j] == v && j < tid);
-    if (above == n - 1) bound = v;
-  }
+  if (tid < groups && is_nth(maxima, groups, tid, n)) bound = maxima[tid];
   __syncthreads();
-  const float least_about = bound;
+  const float least_about = from_order(bound);
   auto put = [&](const Candidate& c) {
     const int at = atomicAdd(&listed, 1);
     if (at < kList) {
@@ -523,25 +699,21 @@ __global__ void __launch_bounds__(kThreads) cache_fork_kernel(const __grid_const
 
 __host__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// How a row is cut: pieces of kThreads x quads x 16 bytes.
+// How a row is cut: as many pieces as fill the SMs' 7 CTAs once, of whole rounds
+// and at most kMaxRounds of them.
 struct Cut {
-  int quads, pieces;
+  int rounds, pieces;
 };
-Cut cut_of(int64_t rows, int V, int size) {
-  const int values = 16 / size;
-  auto pieces = [&](int quads) -> int {
-    const int64_t each = int64_t(kThreads) * quads * values;
-    return static_cast<int>((V + values - 1 + each - 1) / each);
-  };
-  // 128 bytes a thread, or 64 of 16-bit values (32 values either way); where
-  // that leaves SMs without a piece, a quarter
-  const int most = size == 4 ? 8 : 4;
-  const int quads = rows * pieces(most) < sm_count() ? most / 4 : most;
-  return {quads, pieces(quads)};
+Cut cut_of(int64_t rows, int V, int size, bool even) {
+  const int values = 16 / size, each = kThreads * kQuads * values;
+  const int units = (V + (even ? 0 : values - 1) + each - 1) / each;  // (odd: a row's shift)
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(units, sm_count() * 7 / rows));
+  const int rounds = std::min<int>(kMaxRounds, (units + want - 1) / want);
+  return {rounds, (units + rounds - 1) / rounds};
 }
 
 bool beam_sizes_ok(int B, int K, int V, int n) {
-  return n <= kMaxN && int64_t(K) * V < INT_MAX && int64_t(B) * K < (1 << 24);
+  return n <= kMaxN && V <= (1 << 30) && int64_t(K) * V < INT_MAX && int64_t(B) * K < (1 << 24);
 }
 
 }  // namespace
@@ -552,9 +724,10 @@ using namespace dsakv;
 extern "C" size_t ts_beam_workspace_size(int B, int K, int V, int n) {
   if (B <= 0 || K <= 0 || V <= 0 || n <= 0 || !beam_sizes_ok(B, K, V, n)) return 0;
   const int64_t rows = int64_t(B) * K;
-  // (either type's)
-  size_t pieces = std::max(cut_of(rows, V, 4).pieces, cut_of(rows, V, 2).pieces);
-  return align256(rows * sizeof(Beam)) + align256(rows * pieces * sizeof(Piece)) +
+  // (either type's and alignment's)
+  const size_t pieces = std::max(std::max(cut_of(rows, V, 4, false).pieces, cut_of(rows, V, 4, true).pieces),
+                                 std::max(cut_of(rows, V, 2, false).pieces, cut_of(rows, V, 2, true).pieces));
+  return align256(rows * sizeof(Beam)) + align256(rows * pieces * kWarps * sizeof(Piece)) +
          rows * pieces * n * sizeof(uint64_t);
 }
 
@@ -574,28 +747,25 @@ extern "C" ts_status ts_beam_select(const void* logits, int dtype, int64_t row_s
       ws_bytes < ts_beam_workspace_size(B, K, V, n))
     return TS_ERR_WORKSPACE;
   const int64_t rows = int64_t(B) * K;
-  const Cut cut = cut_of(rows, V, size);
-  if (rows * cut.pieces > INT_MAX || int64_t(K) * cut.pieces * n > INT_MAX)
+  const bool even = aligned16(logits) && row_stride * size % 16 == 0;
+  const Cut cut = cut_of(rows, V, size, even);
+  if (rows * cut.pieces > INT_MAX || int64_t(K) * cut.pieces * std::max(n, kWarps) > INT_MAX)
     return TS_ERR_UNSUPPORTED;
   char* w = static_cast<char*>(ws);
   Beam* beams = reinterpret_cast<Beam*>(w);
   w += align256(rows * sizeof(Beam));
   Piece* sums = reinterpret_cast<Piece*>(w);
-  w += align256(rows * cut.pieces * sizeof(Piece));
+  w += align256(rows * cut.pieces * kWarps * sizeof(Piece));
   uint64_t* best = reinterpret_cast<uint64_t*>(w);
-  auto launch = [&](auto kernel, auto* x) {
-    kernel<<<static_cast<unsigned>(rows * cut.pieces), kThreads, 0, stream>>>(
-        x, row_stride, V, n, cut.pieces, best, sums, err);
-  };
-  if (dtype == TS_FP32) {
-    const auto* x = static_cast<const float*>(logits);
-    if (cut.quads == 8) launch(beam_rows_kernel<float, 8>, x);
-    else launch(beam_rows_kernel<float, 2>, x);
-  } else {
-    const auto* x = static_cast<const __nv_bfloat16*>(logits);
-    if (cut.quads == 4) launch(beam_rows_kernel<__nv_bfloat16, 4>, x);
-    else launch(beam_rows_kernel<__nv_bfloat16, 1>, x);
-  }
+  const unsigned grid = static_cast<unsigned>(rows * cut.pieces);
+  const int smem = kThreads * (kStages * kQuads * 16 + cut.rounds * 4);
+  if (dtype == TS_FP32)
+    beam_rows_kernel<<<grid, kThreads, smem, stream>>>(static_cast<const float*>(logits), row_stride,
+                                                       V, n, cut.pieces, cut.rounds, best, sums, err);
+  else
+    beam_rows_kernel<<<grid, kThreads, smem, stream>>>(static_cast<const __nv_bfloat16*>(logits),
+                                                       row_stride, V, n, cut.pieces, cut.rounds,
+                                                       best, sums, err);
   const ts_status st = launch_status();
   if (st != TS_OK) return st;
   return launch_after(beam_merge_kernel, unsigned(B), kThreads, stream, best, sums, cum, K, V, n,

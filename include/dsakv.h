@@ -808,8 +808,8 @@ ts_status sfa_mla_tree(const void* q, int64_t q_stride, const int32_t* cu_q, int
  * sums are 64-bit multiples of 2^-60, as ts_verify_drafts'; probabilities and
  * row sums as there: a bad value sets TS_DEVERR_PROB and counts as 0, a row
  * that adds up to 0, or to 16 or more, sets it too and has -1 for its token.
- * With u NULL a NaN sets TS_DEVERR_NAN and ranks lowest. 0 <= depth <=
- * TS_MAX_TREE, V < 2^23. B = 0 enqueues nothing. */
+ * With u NULL a NaN sets TS_DEVERR_NAN and ranks lowest (a row of NaNs has -1).
+ * 0 <= depth <= TS_MAX_TREE, V <= 2^20. B = 0 enqueues nothing. */
 ts_status ts_verify_tree(const int32_t* tokens, const int32_t* parent, const int32_t* cu_q, int T,
                          int B, const float* target, int64_t target_stride, const float* u, int V,
                          int depth, int32_t* path, int32_t* next, int32_t* accepted, int32_t* err,
@@ -850,7 +850,8 @@ ts_status dsa_cache_keep(void* cache, int64_t num_slots, int fmt, const int32_t*
  *   ws      workspace of ts_beam_workspace_size(B, K, V, n) bytes, 256-byte
  *           aligned, contents need not be preserved; calls that may overlap on
  *           the GPU need one each
- * 1 <= K, 1 <= n <= 128, K * V < 2^31, B * K < 2^24. B = 0 enqueues nothing. */
+ * 1 <= K, 1 <= n <= 64, V <= 2^30, K * V < 2^31 - 1, B * K < 2^24. B = 0
+ * enqueues nothing. */
 #define TS_FP32 0
 #define TS_BF16 1
 size_t ts_beam_workspace_size(int B, int K, int V, int n);
