@@ -86,6 +86,16 @@ struct Layout {
 };
 constexpr int kMaxStages = 7;
 constexpr int kMaxPairs = 80;
+// Trees: where every pair has many key tiles and the requests are few, the pairs
+// take the row tiles in turn, whole ones, and only the last of them are cut. All
+// pairs are then in the same request or two, whose rows stay in L2, where
+// stretches of the line would have them in all requests at once (16 trees of 64
+// nodes x 128 heads over 8192, 151 MB of rows: FIGURES).
+constexpr int kMaxShared = 64, kSharedUnits = 64;
+struct Shared {
+  Request r;
+  int tiles;
+};
 constexpr uint32_t kOCol = 256;  // TMEM columns: S buffers 0..127 and 128..255, O 256..511
 constexpr uint64_t kWaitLimit = 2000000000ull;  // 2 s of global timer per wait
 constexpr uint64_t kDrainNs = 2000000ull;
@@ -124,6 +134,7 @@ struct Bars {
   int abort;
   int start_b, start_j, start_u;  // where the pair's stretch of work begins
   int64_t count;                  // and its length in units
+  int rounds;                     // whole row tiles before it
   float red[2][2][kRows];         // exchange between a row's threads
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
@@ -170,6 +181,7 @@ __device__ __forceinline__ Request request(const Args& a, int b) {
 
 // The pair's stretch of the line of all units: thread-per-request sums, then
 // the request, row tile and key tile that the stretch begins in.
+template <bool kTree>
 __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   auto units_of = [&](int b) -> int64_t {
@@ -202,7 +214,50 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
   for (int b = tid; b < a.B; b += threads) mine += units_of(b);
   int64_t inc = scan(mine, &total);
   const Stretch st = stretch_of(total, a.pairs, pair);
-  const int64_t from = st.from, count = st.count;
+  int64_t from = st.from, count = st.count;
+  if (kTree) {
+    if (tid == 0) bars->rounds = 0;
+    if (a.B <= kMaxShared && total >= int64_t(kSharedUnits) * a.pairs && total < INT_MAX) {
+      Shared s = {};
+      if (tid < a.B) {
+        s.r = request(a, tid);
+        s.tiles = row_tiles(a.H, s.r);
+      }
+      int64_t tiles;
+      const int first = static_cast<int>(scan(s.tiles, &tiles)) - s.tiles;
+      int* const firsts = reinterpret_cast<int*>(bars->red);
+      int *units = firsts + kMaxShared + 1, *load = units + kMaxShared;
+      static_assert((2 * kMaxShared + 1 + kMaxPairs) * sizeof(int) <= sizeof(bars->red), "scratch");
+      if (tid < a.B) {
+        firsts[tid] = first;
+        units[tid] = key_tiles(s.r.ctx);
+      }
+      if (tid == 0) firsts[a.B] = static_cast<int>(tiles);
+      for (int p = tid; p < a.pairs; p += threads) load[p] = 0;
+      __syncthreads();
+      const int rounds = static_cast<int>(tiles) / a.pairs - 1;
+      for (int i = tid; rounds > 0 && i < a.B * a.pairs; i += threads) {
+        const int b = i / a.pairs, p = i - b * a.pairs;
+        const int mine = round_tiles(a.pairs, rounds, p, firsts[b], firsts[b + 1]);
+        if (mine) atomicAdd(&load[p], mine * units[b]);
+      }
+      __syncthreads();
+      bool fits = rounds > 0;
+      for (int p = tid; p < a.pairs; p += threads)
+        fits = fits && load[p] < stretch_of(total, a.pairs, p).count;
+      if (__syncthreads_and(fits)) {
+        int64_t mine_load = 0, all_load;
+        if (tid < a.pairs) mine_load = load[tid];
+        scan(mine_load, &all_load);
+        int64_t before = 0;  // of the pairs before this one
+        for (int p = 0; p < pair; ++p) before += load[p];
+        from = all_load + (st.from - before);
+        count = st.count - load[pair];
+        if (tid == 0) bars->rounds = rounds;
+      }
+      __syncthreads();
+    }
+  }
   if (tid == 0) bars->count = count;
   int64_t base = 0;
 #pragma unroll 1
@@ -224,6 +279,38 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
   }
   __syncthreads();
 }
+
+// A pair's row tiles and key tiles: of a tree, first its whole row tiles.
+template <bool kTree>
+struct Walker {
+  Walk walk;
+  int rounds, pairs, b, j;
+  __device__ __forceinline__ Walker(const Args& a, const Bars* bars, int pair)
+      : walk{bars->start_b, bars->start_j, bars->start_u, bars->count},
+        rounds(kTree ? bars->rounds : 0),
+        pairs(a.pairs),
+        b(0),
+        j(pair) {}
+  __device__ __forceinline__ bool next(const Args& a, Segment& s) {
+    if (!kTree || rounds == 0) return walk.next(a, s);
+    --rounds;
+    for (;; ++b) {  // (there are that many row tiles)
+      s.r = request(a, b);
+      const int tiles = row_tiles(a.H, s.r);
+      if (j < tiles) break;
+      j -= tiles;
+    }
+    s.b = b;
+    s.row0 = j * kRows;
+    s.rows = static_cast<int>(least(int64_t(kRows), int64_t(s.r.n) * a.H - s.row0));
+    s.end = s.r.ctx;
+    s.t0 = 0;
+    s.t1 = key_tiles(s.end);
+    s.starts = s.ends = true;
+    j += pairs;
+    return true;
+  }
+};
 
 // Reports lengths out of range (once per launch).
 __device__ __forceinline__ void check_lengths(const Args& a) {
@@ -459,7 +546,8 @@ __device__ __forceinline__ int stages_of(const Segment& g, int t) {
 // that a row's nine pieces come from there, made every case slower: the long
 // prefetches hold the TMA unit up. 32 x 32,768 positions, one token: 402 us
 // with them, 269 without.)
-__device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
+template <class W>
+__device__ __forceinline__ void load_bf16(Loader& ld, W walk, int w) {
   constexpr int kStages = Layout<DSA_CACHE_BF16>::kStages;
   const Args& a = ld.a;
   Segment sg;
@@ -517,7 +605,8 @@ __device__ __forceinline__ void load_bf16(Loader& ld, Walk walk, int w) {
 // 8-bit rows: walks the pair's work for the converting warps, which have too
 // few registers for it (what they spill comes back at L2's distance: nearly all
 // of the L1 is shared memory here), and loads Q.
-__device__ __forceinline__ void load_q_8bit(Loader& ld, Walk walk) {
+template <class W>
+__device__ __forceinline__ void load_q_8bit(Loader& ld, W walk) {
   const Args& a = ld.a;
   Bars* bars = ld.bars;
   Segment sg;
@@ -796,7 +885,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
   tc_fence_before();
   cluster_arrive();
   if (blockIdx.x == 0) check_lengths(a);
-  plan(a, bars, pair);
+  plan<kTree>(a, bars, pair);
   cluster_wait();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_slot;
@@ -806,7 +895,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
     return Loader{a, maps, bars, q_tile, ring, raw, rank, dsmem_addr(&bars->q_full, 0),
                   dsmem_addr(&bars->full[0], 0), lane, elect_one(), abort, k_step, min(4, k_step)};
   };
-  Walk walk{bars->start_b, bars->start_j, bars->start_u, bars->count};
+  Walker<kTree> walk(a, bars, pair);
   Segment sg;
   if (warp < kSoftmaxWarps) {
     // ---------------- softmax and epilogue: kParts threads per TMEM lane ----------------

@@ -83,6 +83,15 @@ PLAN_INLINE Stretch stretch_of(int64_t total, int max_pairs, int pair) {
   return {share * pair + least(pair, more), pair < pairs ? share + (pair < more ? 1 : 0) : 0};
 }
 
+// Row tiles first .. last - 1 of the line of all row tiles that pair p takes when
+// `pairs` pairs take them in turn, `rounds` each.
+PLAN_INLINE int round_tiles(int pairs, int rounds, int p, int first, int last) {
+  auto below = [&](int x) {  // those numbers i < x with i % pairs = p
+    return least(rounds, (x - p + pairs - 1) / pairs);
+  };
+  return below(last) - below(first);
+}
+
 // The row tile and key tile of a request that its unit `at` is: the last row
 // tile that begins at or before it.
 struct Place {
