@@ -463,8 +463,9 @@ class DecodeGroup:
 
 
 class PagedKV:
-    """The paged latent cache of one layer (dsa_cache_write, dsa_cache_read,
-    sfa_mla_chunk): num_pages pages of page_size rows, as bf16 or quantised to
+    """The paged latent cache of one layer (dsa_cache_write, dsa_cache_append,
+    dsa_cache_read, sfa_mla_chunk, sfa_mla_tree, dsa_cache_keep,
+    dsa_cache_fork): num_pages pages of page_size rows, as bf16 or quantised to
     8 bits (fmt "e4m3"). The caller deals out the pages; a request's position t
     lies in slot block_table[b][t // page_size] * page_size + t % page_size.
     `data` are the rows (uint8 [num_pages * page_size][row bytes]), `err` the
@@ -526,6 +527,156 @@ class PagedKV:
                 rope.stride(0) if n > 1 else D - DV, slots, n, self.data, self.num_slots,
                 self._fmt, self.err, self._stream(stream, self.data.device)), "dsa_cache_write")
 
+    def append(self, latent: torch.Tensor, rope: torch.Tensor, pos: torch.Tensor,
+               slots: torch.Tensor, freq: torch.Tensor, q_rope: torch.Tensor | None = None,
+               q: torch.Tensor | None = None, interleaved: bool = True, stream=None) -> None:
+        """write, with the rope parts turned by their positions on the way: pos
+        int32 [n], freq float64 [32] (radians a position), pairs of values side by
+        side (interleaved) or half the part apart. With q_rope [n][H][64] (bf16,
+        tokens and heads of any stride) the queries' rope parts are turned too,
+        into q[..., 512:] (bf16 [n][H][576], a token's heads contiguous); q_rope
+        may be that part itself."""
+        n = latent.shape[0]
+        rope_dim = D - DV
+        self._bf16(latent, "latent", (n, DV))
+        self._bf16(rope, "rope", (n, rope_dim))
+        for t, name in ((pos, "pos"), (slots, "slots")):
+            if self._int32(t, name, 1).shape[0] != n:
+                raise ValueError(f"{name}: one for each row")
+        if (freq.dtype != torch.float64 or tuple(freq.shape) != (rope_dim // 2,)
+                or not freq.is_contiguous() or freq.device != self.data.device):
+            raise ValueError(f"freq: expected contiguous float64 {(rope_dim // 2,)} on "
+                             f"{self.data.device}")
+        if (q_rope is None) != (q is None):
+            raise ValueError("q_rope, q: both or neither")
+        H, strides = 0, (0, 0, 0)
+        if q is not None:
+            H = q.shape[1] if q.dim() == 3 else 0
+            self._bf16(q, "q", (n, H, D))
+            self._bf16(q_rope, "q_rope", (n, H, rope_dim))
+            if n and H and (q.stride(2) != 1 or (H > 1 and q.stride(1) != D)):
+                raise ValueError("q: a token's heads must be contiguous")
+            if n and H and q_rope.stride(2) != 1:
+                raise ValueError("q_rope: a head's values must be contiguous")
+            # (a dimension of one may have any stride)
+            head = q_rope.stride(1) if H > 1 else rope_dim
+            strides = (q_rope.stride(0) if n > 1 else rope_dim, head,
+                       q.stride(0) if n > 1 else H * D)
+        if n == 0:
+            return
+        if latent.stride(1) != 1 or rope.stride(1) != 1:
+            raise ValueError("latent, rope: rows must be contiguous")
+        if H == 0:
+            q_rope = None
+        with torch.cuda.device(self.data.device):
+            abi.check(abi.dsa_cache_append(
+                latent, latent.stride(0) if n > 1 else DV, rope,
+                rope.stride(0) if n > 1 else rope_dim, pos, slots, n, freq, interleaved,
+                self.data, self.num_slots, self._fmt, q_rope, strides[0], strides[1], H, q,
+                strides[2], self.err, self._stream(stream, self.data.device)), "dsa_cache_append")
+
+    def plan_tree(self, parent: torch.Tensor | None, cu_q: torch.Tensor,
+                  block_table: torch.Tensor, ctx_len: torch.Tensor, T: int, most: int,
+                  stream=None):
+        """What append and attend need of a step's drafted trees (dsa_tree_plan):
+        parent int32 [T] (a node's parent's number within its request, -1 for a
+        root; None: chains), at most `most` nodes a request. Returns (pos int32
+        [T], slots int32 [T], mask int32 [T][ceil(most / 32)]); the same for every
+        layer's cache of these pages."""
+        B = ctx_len.shape[0]
+        if T < 0 or not 1 <= most <= abi.TS_MAX_TREE:
+            raise ValueError(f"T, most: at least 0, and 1 to {abi.TS_MAX_TREE}")
+        if parent is not None and self._int32(parent, "parent", 1).shape[0] != T:
+            raise ValueError("parent: one for each token")
+        if self._int32(cu_q, "cu_q", 1).shape[0] != B + 1:
+            raise ValueError("cu_q: one more than the requests")
+        self._table(block_table, ctx_len, B)
+        dev, words = self.data.device, -(-most // 32)
+        if T == 0:
+            new = dict(dtype=torch.int32, device=dev)
+            return torch.empty(0, **new), torch.empty(0, **new), torch.empty((0, words), **new)
+        st = self._stream(stream, dev)
+        with torch.cuda.device(dev), torch.cuda.stream(st):
+            pos = torch.empty((T,), dtype=torch.int32, device=dev)
+            slots = torch.empty((T,), dtype=torch.int32, device=dev)
+            mask = torch.empty((T, words), dtype=torch.int32, device=dev)
+            if B:
+                abi.check(abi.dsa_tree_plan(parent, cu_q, T, B, ctx_len, block_table,
+                                            self._table_stride(block_table), self.page_size,
+                                            self.num_slots, pos, slots, mask, words, self.err, st),
+                          "dsa_tree_plan")
+            else:  # tokens that no request has
+                pos.zero_(), slots.fill_(-1), mask.zero_()
+        return pos, slots, mask
+
+    def keep(self, path: torch.Tensor, accepted: torch.Tensor, cu_q: torch.Tensor, T: int,
+             block_table: torch.Tensor, ctx_len: torch.Tensor, new_len: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+        """The rows of verify_tree's accepted paths moved together behind each
+        request's context (dsa_cache_keep): path int32 [B][depth + 1], accepted
+        int32 [B]; cu_q, T and ctx_len as in the step's attention. Returns the
+        requests' lengths afterwards (new_len int32 [B], a fresh one unless given;
+        it may be ctx_len)."""
+        dev, B = self.data.device, ctx_len.shape[0]
+        self._table(block_table, ctx_len, B)
+        if not self._int32(path, "path", 2).is_contiguous() or path.shape[0] != B or \
+                path.shape[1] < 1:
+            raise ValueError("path: a contiguous row for each request")
+        if self._int32(cu_q, "cu_q", 1).shape[0] != B + 1:
+            raise ValueError("cu_q: one more than the requests")
+        if T < 0:
+            raise ValueError("T: at least 0")
+        for t, name in ((accepted, "accepted"), (new_len, "new_len")):
+            if t is not None and self._int32(t, name, 1).shape[0] != B:
+                raise ValueError(f"{name}: one for each request")
+        if B == 0:
+            return torch.empty(0, dtype=torch.int32, device=dev) if new_len is None else new_len
+        st = self._stream(stream, dev)
+        with torch.cuda.device(dev), torch.cuda.stream(st):
+            if new_len is None:
+                new_len = torch.empty((B,), dtype=torch.int32, device=dev)
+            abi.check(abi.dsa_cache_keep(
+                self.data, self.num_slots, self._fmt, block_table,
+                self._table_stride(block_table), self.page_size, cu_q, T, ctx_len, B, path,
+                path.shape[1] - 1, accepted, new_len, self.err, st), "dsa_cache_keep")
+        return new_len
+
+    def fork(self, parents: torch.Tensor, spare: torch.Tensor, block_table: torch.Tensor,
+             ctx_len: torch.Tensor, tables: bool = True, stream=None):
+        """The sequences' states in beam_select's new order (dsa_cache_fork):
+        parents int32 [B][n] (the beam each continues, -1: none) over the B * K
+        sequences of block_table and ctx_len; spare int32 [B * n]: a page of its own
+        for each new sequence, which gets the rows of its parent's partial last page
+        and the rows to come. Returns (block_table int32 [B * n][..], ctx_len int32
+        [B * n]) of the new sequences; `tables` False: the rows alone (the other
+        layers' caches), and None."""
+        dev = self.data.device
+        B, n = self._int32(parents, "parents", 2).shape
+        old = ctx_len.shape[0]
+        self._table(block_table, ctx_len, old)
+        if not parents.is_contiguous():
+            raise ValueError("parents must be contiguous")
+        if self._int32(spare, "spare", 1).shape[0] != B * n:
+            raise ValueError("spare: one for each new sequence")
+        if B and old % B:
+            raise ValueError("block_table, ctx_len: equally many sequences for each request")
+        def made():
+            if not tables:
+                return None, None
+            new = dict(dtype=torch.int32, device=dev)
+            return torch.empty((B * n, block_table.shape[1]), **new), torch.empty(B * n, **new)
+
+        if B == 0 or n == 0:
+            return made() if tables else None
+        st = self._stream(stream, dev)
+        with torch.cuda.device(dev), torch.cuda.stream(st):
+            table, length = made()
+            abi.check(abi.dsa_cache_fork(
+                self.data, self.num_slots, self._fmt, block_table,
+                self._table_stride(block_table), self.page_size, ctx_len, parents, spare, B,
+                old // B, n, table, length, self.err, st), "dsa_cache_fork")
+        return (table, length) if tables else None
+
     def read(self, block_table: torch.Tensor, ctx_len: torch.Tensor, pos: torch.Tensor,
              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The rows of positions pos [B][k] as bf16 [B][k][576]: sfa_mla_decode's
@@ -564,7 +715,7 @@ class PagedKV:
     def attend(self, q: torch.Tensor, cu_q: torch.Tensor, block_table: torch.Tensor,
                ctx_len: torch.Tensor, causal: bool = True, scale: float | None = None,
                out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-               ws: torch.Tensor | None = None, stream=None):
+               ws: torch.Tensor | None = None, stream=None, tree: torch.Tensor | None = None):
         """Attention of the newest tokens q [T][H][576] (request b's are rows
         cu_q[b] .. cu_q[b + 1]) over the cached positions below ctx_len[b];
         block_table int32 [B][pages a request], contiguous. Returns (out bf16
@@ -572,7 +723,9 @@ class PagedKV:
         request has are left as they were. `ws`: a workspace of
         `workspace(T, B, H)` kept by the caller (contiguous uint8 on the cache's
         device); without one the call takes its own from PyTorch's allocator, on
-        its stream."""
+        its stream. `tree`: the new tokens are drafted trees, and of the new
+        positions each sees those of its row of plan_tree's masks (int32
+        [T][words], sfa_mla_tree; `causal` is not used then)."""
         dev = self.data.device
         T, H = q.shape[0], q.shape[1]
         B = ctx_len.shape[0]
@@ -591,6 +744,9 @@ class PagedKV:
         if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, H)
                                 or not lse.is_contiguous() or lse.device != dev):
             raise ValueError(f"lse: expected contiguous float32 {(T, H)} on {dev}")
+        if tree is not None and (self._int32(tree, "tree", 2).shape[0] != T
+                                 or not tree.is_contiguous() or not tree.shape[1]):
+            raise ValueError("tree: a contiguous row of masks for each token")
         if (T == 0 or B == 0) and out is not None and lse is not None:
             return out, lse
         st = self._stream(stream, dev)
@@ -603,11 +759,15 @@ class PagedKV:
                 return out, lse
             if ws is None:
                 ws = self.workspace(T, B, H)
-            abi.check(abi.sfa_mla_chunk(
-                q, q.stride(0) if T > 1 else H * D, cu_q, T, B, H, self.data, self.num_slots,
-                self._fmt, block_table, self._table_stride(block_table), self.page_size, ctx_len,
-                causal, 1.0 / math.sqrt(D) if scale is None else scale, out, lse, ws, ws.numel(),
-                self.err, st), "sfa_mla_chunk")
+            first = (q, q.stride(0) if T > 1 else H * D, cu_q, T, B, H, self.data,
+                     self.num_slots, self._fmt, block_table, self._table_stride(block_table),
+                     self.page_size, ctx_len)
+            last = (1.0 / math.sqrt(D) if scale is None else scale, out, lse, ws, ws.numel(),
+                    self.err, st)
+            if tree is None:
+                abi.check(abi.sfa_mla_chunk(*first, causal, *last), "sfa_mla_chunk")
+            else:
+                abi.check(abi.sfa_mla_tree(*first, tree, tree.shape[1], *last), "sfa_mla_tree")
         return out, lse
 
     def workspace(self, T: int, B: int, H: int) -> torch.Tensor:
@@ -661,3 +821,84 @@ def verify_drafts(drafts: torch.Tensor, target: torch.Tensor, draft: torch.Tenso
         abi.check(abi.ts_verify_drafts(drafts, n_draft, target, ts, draft, ds, u, B, n, V, tokens,
                                        accepted, err, st), "ts_verify_drafts")
     return tokens, accepted
+
+
+def verify_tree(tokens: torch.Tensor, parent: torch.Tensor | None, cu_q: torch.Tensor,
+                target: torch.Tensor, u: torch.Tensor | None, depth: int | None = None,
+                err: torch.Tensor | None = None, stream=None):
+    """ts_verify_tree on tensors: drafted trees, tokens int32 [T] and parent int32
+    [T] (None: chains), packed by cu_q int32 [B + 1], against target float [T][V],
+    by u float [B][depth + 1], or (u None, with depth) by the largest value. Returns
+    (path int32 [B][depth + 1], tokens int32 [B][depth + 1], accepted int32 [B]).
+    `err`: a device error word (int32 [1], read with ts_read_error); without one bad
+    probabilities are not reported."""
+    dev = target.device
+    if target.dim() != 2 or cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        raise ValueError("target, cu_q: expected [T][V] and [B + 1]")
+    (T, V), B = target.shape, cu_q.shape[0] - 1
+    if u is not None and (u.dim() != 2 or u.shape[1] < 1):
+        raise ValueError("u: expected [B][depth + 1]")
+    if depth is None:
+        if u is None:
+            raise ValueError("depth: needed without u")
+        depth = u.shape[1] - 1
+    if depth < 0:
+        raise ValueError("depth: at least 0")
+    if (target.dtype != torch.float32 or (V > 1 and T and target.stride(1) != 1)
+            or (T > 1 and target.stride(0) < V)):
+        raise ValueError("target: expected float32 rows, V floats or more apart")
+    for t, name, dtype, shape in ((tokens, "tokens", torch.int32, (T,)),
+                                  (parent, "parent", torch.int32, (T,)),
+                                  (cu_q, "cu_q", torch.int32, (B + 1,)),
+                                  (u, "u", torch.float32, (B, depth + 1)),
+                                  (err, "err", torch.int32, (1,))):
+        if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or t.device != dev
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name}: expected contiguous {dtype} {shape} on {dev}")
+    st = torch.cuda.current_stream(dev) if stream is None else stream
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        path = torch.empty((B, depth + 1), dtype=torch.int32, device=dev)
+        out = torch.empty((B, depth + 1), dtype=torch.int32, device=dev)
+        accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+        abi.check(abi.ts_verify_tree(tokens, parent, cu_q, T, B, target,
+                                     target.stride(0) if T > 1 else V, u, V, depth, path, out,
+                                     accepted, err, st), "ts_verify_tree")
+    return path, out, accepted
+
+
+def beam_select(logits: torch.Tensor, cum: torch.Tensor, n: int, ws: torch.Tensor | None = None,
+                err: torch.Tensor | None = None, stream=None):
+    """ts_beam_select on tensors: the n best continuations of each request's K
+    beams, logits float32 or bf16 [B][K][V] (rows evenly spaced), cum float [B][K].
+    Returns (tokens int32 [B][n], parents int32 [B][n], scores float [B][n]).
+    `ws`: a workspace of ts_beam_workspace_size(B, K, V, n) bytes kept by the
+    caller (contiguous uint8); `err`: a device error word (int32 [1])."""
+    dev = logits.device
+    if logits.dim() != 3 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits: expected float32 or bf16 [B][K][V]")
+    B, K, V = logits.shape
+    # (a dimension of one may have any stride)
+    step = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
+    if logits.numel() and ((V > 1 and logits.stride(2) != 1) or step < V
+                           or (B > 1 and K > 1 and logits.stride(0) != K * step)):
+        raise ValueError("logits: its rows must be evenly spaced, V values or more apart")
+    for t, name, dtype, shape in ((cum, "cum", torch.float32, (B, K)),
+                                  (err, "err", torch.int32, (1,))):
+        if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or t.device != dev
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name}: expected contiguous {dtype} {shape} on {dev}")
+    # (its size and alignment are the library's to check)
+    if ws is not None and (ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws: expected contiguous uint8 on {dev}")
+    st = torch.cuda.current_stream(dev) if stream is None else stream
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        tokens = torch.empty((B, n), dtype=torch.int32, device=dev)
+        parents = torch.empty((B, n), dtype=torch.int32, device=dev)
+        scores = torch.empty((B, n), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = torch.empty((max(256, abi.ts_beam_workspace_size(B, K, V, n)),),
+                             dtype=torch.uint8, device=dev)
+        abi.check(abi.ts_beam_select(logits, abi.TS_FP32 if logits.dtype == torch.float32
+                                     else abi.TS_BF16, step, cum, B, K, V, n, tokens, parents,
+                                     scores, ws, ws.numel(), err, st), "ts_beam_select")
+    return tokens, parents, scores

@@ -720,7 +720,7 @@ ts_status ts_verify_drafts(const int32_t* drafts, const int32_t* n_draft, const 
  * cached at the request's position ctx_len[b] - n + i (ctx_len counts them).
  * Node i's parent is a node of a lower number of the same request, or -1: a
  * root, which follows the cached context. A request has at most TS_MAX_TREE
- * nodes. cu_q ascends and ctx_len[b] >= n; TS_DEVERR_ORDER and TS_DEVERR_CTX
+ * nodes (chains given without parents: any number). cu_q ascends and ctx_len[b] >= n; TS_DEVERR_ORDER and TS_DEVERR_CTX
  * report where they do not, with the values then taken as sfa_mla_chunk's.
  * ------------------------------------------------------------------------- */
 #define TS_MAX_TREE 1024
@@ -760,10 +760,11 @@ ts_status dsa_tree_plan(const int32_t* parent, const int32_t* cu_q, int T, int B
  *                                   queries. It may be q's own part.
  *   q      bf16 [n][H][576]         its values 512..575 are written, tokens q_stride apart
  *                                   (>= H * 576, a multiple of 8; 16-byte aligned)
- * The angle is reduced exactly, whatever the position: pos times freq / 2 pi to
- * 2^-64 of a turn. Sine and cosine are fp32, the values round once to bf16. A row whose slot
- * is negative, or past the cache (TS_DEVERR_SLOT_RANGE), is skipped; its
- * queries are turned all the same. n = 0 enqueues nothing. */
+ * The angle is reduced in whole 2^-64 turns: for |freq| <= 1 it is off by at
+ * most |pos| 2^-54 of a turn, and then by its rounding to fp32. Sine and cosine
+ * are fp32, the values round once to bf16. A row whose slot is negative, or past
+ * the cache (TS_DEVERR_SLOT_RANGE), is skipped; its queries are turned all the
+ * same. n = 0 enqueues nothing. */
 ts_status dsa_cache_append(const void* latent, int64_t latent_stride, const void* rope,
                            int64_t rope_stride, const int32_t* pos, const int32_t* slots, int n,
                            const double* freq, int pairs, void* cache, int64_t num_slots, int fmt,

@@ -28,3 +28,4 @@ from .install import dsa_install, metadata_update
 from .sfa import bf16_bits_to_f64, round_to_bf16_bits, sfa_decode
 from .step import RequestState, decode_step, init_state
 from .paged import chunk_attention, pack_row, unpack_row, verify_drafts
+from . import candidates
