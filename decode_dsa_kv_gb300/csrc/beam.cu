@@ -156,10 +156,10 @@ struct Quad<__nv_bfloat16> {
   }
 };
 
-// Threads whose maximum is a group's: as many groups as a power of two from 4 n
-// on, or (n above 32) from 2 n on.
-__host__ __device__ inline int group_threads(int n) {
-  return n <= 8 ? 4 : n <= 16 ? 2 : 1;
+// Threads of a CTA's whose maximum is a group's: as many groups as a power of two
+// from 4 n on, or as there are threads (n above 32: from 2 n on).
+__device__ __forceinline__ int group_threads(int threads, int n) {
+  return max(1, threads / (n <= 8 ? 32 : n <= 16 ? 64 : n <= 32 ? 128 : 256));
 }
 
 // The n-th largest of the first `groups` words of `of` (all different, or equal
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 7)
   }
 
   // ---- the n best ----
-  const int per = group_threads(n), groups = kThreads / per;
+  const int per = group_threads(kThreads, n), groups = kThreads / per;
   {
     uint32_t m = in_order(mine);
     for (int d = 1; d < per; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -436,22 +436,49 @@ struct Candidate {
   }
 };
 
+// log s of s >= 2^-30, within 2^-29 (2^25 values tried): s = 2^k c (1 + r) with c a float of
+// [1/sqrt 2, sqrt 2] and |r| below 2^-24, log c = 2 artanh(q), q = (c - 1) / (c +
+// 1), of which only q itself needs two floats. (CUDA's own of a double takes 1.2
+// us here, where fp64 is slow: a third of the kernel.)
+__device__ __forceinline__ double log_of(double s) {
+  int k = static_cast<int>(static_cast<uint64_t>(__double_as_longlong(s)) >> 52) - 1023;
+  double f = __longlong_as_double((__double_as_longlong(s) & 0xfffffffffffffll) |
+                                  0x3ff0000000000000ll);  // in [1, 2)
+  if (f > 1.41421356) {
+    f *= 0.5;
+    ++k;
+  }
+  const float c = static_cast<float>(f), r = static_cast<float>(f - double(c)) / c;
+  const float above = c - 1.f, below = c + 1.f;  // (the first is exact)
+  const float low = c < 1.f ? c - (below - 1.f) : 1.f - (below - c);  // what the second lost
+  const float q = above / below;
+  const float rest = fmaf(-q, low, fmaf(-q, below, above)) / below;
+  const float q2 = q * q;
+  // 1/3 + q2 / 5 + .. (q2 < 0.0295: the next term is below 2^-37 of q)
+  const float series =
+      fmaf(q2, fmaf(q2, fmaf(q2, fmaf(q2, fmaf(q2, 1.f / 13, 1.f / 11), 1.f / 9), 1.f / 7), 0.2f),
+           1.f / 3);
+  const float small = fmaf(2.f, fmaf(q * q2, series, rest), r);
+  return k * kLn2 + (2.0 * q + small);
+}
+
 // A beam: a continuation's score is (x - m) + rest.
 struct Beam {
   double m, rest;
 };
 
 // One CTA a request. Its time is its chain: the pieces' sums and best, which are
-// all on their way from the start, a logarithm for each beam (fp64, all beams at
-// once), and three barriers.
+// all on their way from the start, a logarithm for each beam, and the barriers
+// between those, the bound, the list and the places.
+constexpr int kMergeThreads = 256;
 constexpr int kAhead = 4;  // candidates a thread holds in registers
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kMergeThreads)
     beam_merge_kernel(const uint64_t* best, const Piece* sums, const float* cum, int K, int V,
                       int n, int pieces, Beam* beams, int32_t* tokens, int32_t* parents,
                       float* scores, int32_t* err) {
   __shared__ uint64_t score[kList];
   __shared__ uint32_t place[kList];
-  __shared__ __align__(16) uint32_t maxima[kThreads];
+  __shared__ __align__(16) uint32_t maxima[kMergeThreads];
   __shared__ uint32_t bound;
   __shared__ int listed;
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -463,14 +490,14 @@ __global__ void __launch_bounds__(kThreads)
   uint64_t ahead[kAhead];
 #pragma unroll
   for (int j = 0; j < kAhead; ++j) {
-    const uint32_t i = tid + j * kThreads;
+    const uint32_t i = tid + j * kMergeThreads;
     ahead[j] = i < all ? best[i] : 0;
   }
   if (tid == 0) listed = 0;
   // every beam's sum of exponentials, in whole multiples of 2^-30 of 2^e: a warp
   // a beam
   beams += int64_t(b) * K;
-  for (int k = warp; k < K; k += kWarps) {
+  for (int k = warp; k < K; k += kMergeThreads / 32) {
     const int parts = pieces * kWarps;
     const Piece* of = sums + (int64_t(b) * K + k) * parts;
     Piece first = {0.f, 0, 0.f};
@@ -515,9 +542,9 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   __syncthreads();
-  for (int k = tid; k < K; k += kThreads) {
+  for (int k = tid; k < K; k += kMergeThreads) {
     const double s = beams[k].rest;
-    beams[k].rest = s > 0 ? double(cum[int64_t(b) * K + k]) - log(s) : -INFINITY;
+    beams[k].rest = s > 0 ? double(cum[int64_t(b) * K + k]) - log_of(s) : -INFINITY;
   }
   __syncthreads();
   auto walk = [&](auto&& f) {
@@ -528,8 +555,8 @@ __global__ void __launch_bounds__(kThreads)
     };
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
-      if (ahead[j]) one(tid + j * kThreads, ahead[j]);
-    for (uint32_t i = tid + kAhead * kThreads; i < all; i += kThreads) one(i, best[i]);
+      if (ahead[j]) one(tid + j * kMergeThreads, ahead[j]);
+    for (uint32_t i = tid + kAhead * kMergeThreads; i < all; i += kMergeThreads) one(i, best[i]);
   };
   auto candidate = [&](int k, const Beam& beam, uint64_t key) -> Candidate {
     const double x = from_order(static_cast<uint32_t>(key >> 32));
@@ -553,7 +580,7 @@ __global__ void __launch_bounds__(kThreads)
     const float y = about(beam, key, &off);
     mine = fmaxf(mine, y - off);
   });
-  const int per = group_threads(n), groups = kThreads / per;
+  const int per = group_threads(kMergeThreads, n), groups = kMergeThreads / per;
   for (int d = 1; d < per; d <<= 1)
     mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, d));
   if (tid % per == 0) maxima[tid / per] = in_order(mine);
@@ -615,7 +642,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   const int count = min(listed, kList);
   const int64_t out = int64_t(b) * n;
-  for (int i = tid; i < count; i += kThreads) {
+  for (int i = tid; i < count; i += kMergeThreads) {
     const Candidate c = {score[i], place[i]};
     int above = 0;
     for (int j = 0; j < count; ++j) above += Candidate{score[j], place[j]}.above(c);
@@ -625,7 +652,7 @@ __global__ void __launch_bounds__(kThreads)
     parents[out + above] = static_cast<int>(at / V);
     scores[out + above] = static_cast<float>(from_order64(c.score));
   }
-  for (int i = count + tid; i < n; i += kThreads) {
+  for (int i = count + tid; i < n; i += kMergeThreads) {
     tokens[out + i] = parents[out + i] = -1;
     scores[out + i] = -INFINITY;
   }
@@ -768,7 +795,7 @@ extern "C" ts_status ts_beam_select(const void* logits, int dtype, int64_t row_s
                                                        best, sums, err);
   const ts_status st = launch_status();
   if (st != TS_OK) return st;
-  return launch_after(beam_merge_kernel, unsigned(B), kThreads, stream, best, sums, cum, K, V, n,
+  return launch_after(beam_merge_kernel, unsigned(B), kMergeThreads, stream, best, sums, cum, K, V, n,
                       cut.pieces, beams, tokens, parents, scores, err);
 }
 
