@@ -5,7 +5,7 @@
 namespace dsakv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeads = 16;  // of a warp's share of a token's queries
 
@@ -95,8 +95,9 @@ struct Args {
 template <int kFmt, bool kPairs>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ Args a) {
   const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int row = static_cast<int>(item / a.shares), share = static_cast<int>(item % a.shares);
+  const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);  // (below 2^32)
+  const int row = static_cast<int>(item / uint32_t(a.shares));
+  const int share = static_cast<int>(item - uint32_t(row) * a.shares);
   wait_previous_kernel();
   if (row >= a.n) return;
   const int pos = a.pos[row];
@@ -191,7 +192,7 @@ extern "C" ts_status dsa_cache_append(const void* latent, int64_t latent_stride,
   a.q_stride = q_stride;
   a.err = err;
   const int64_t blocks = (int64_t(n) * a.shares + kWarps - 1) / kWarps;
-  if (blocks > 2147483647) return TS_ERR_UNSUPPORTED;
+  if (blocks * kWarps > 0xffffffffll) return TS_ERR_UNSUPPORTED;
   auto kernel = fmt == DSA_CACHE_BF16 ? (pairs ? cache_append_kernel<DSA_CACHE_BF16, true>
                                                : cache_append_kernel<DSA_CACHE_BF16, false>)
                                       : (pairs ? cache_append_kernel<DSA_CACHE_E4M3, true>
