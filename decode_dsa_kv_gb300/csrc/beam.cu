@@ -20,6 +20,12 @@
 // join exactly, by powers of two, and no rounding of a maximum, which the whole
 // row would share, enters the result. (Where a warp's largest value is past 2^20
 // in size, rows of a type's lowest value, m is that value itself.)
+//
+// Measured: 64 x 8 beams over 131,072 bf16 logits (134 MB) 35 us, 0.57 of the
+// measured copy rate: the stream alone is 25, a piece's end (reductions, bound,
+// the hits' second reading, places) some 3 us of which other pieces hide a part,
+// the merge 4 behind it. 16 x 10 over 50,257 fp32 (32 MB) 16.1 us; 1 x 4 over
+// 32,000 8 us, its two launches and their chains.
 #include <algorithm>
 #include <climits>
 
@@ -180,7 +186,8 @@ __device__ __forceinline__ bool is_nth(const uint32_t* of, int groups, int i, in
 // A piece is `rounds` rounds of kQuads 16-byte loads a thread. They go through
 // shared memory, each thread's through places of its own, so that the next two
 // rounds are on their way without a register (in registers, one round ahead, the
-// compiler spilled: 64 against 58 us for the version that read no ahead).
+// compiler spilled: 64 x 8 over 131,072 took 64 us where this took 50). 8 rounds at
+// most: 30.9 us for the kernel, 34.7 with 4 and 35.2 with 16.
 template <class T>
 __global__ void __launch_bounds__(kThreads, 7)
     beam_rows_kernel(const T* __restrict__ logits, int64_t row_stride, int V, int n, int pieces,
@@ -660,8 +667,10 @@ __global__ void __launch_bounds__(kMergeThreads)
 
 // ---------------------------------------------------------------------------
 // A page's rows lie side by side, so a partial last page is one copy of whole
-// 16-byte pieces. A CTA takes 16 KB of a sequence's; the first writes its table
-// row too.
+// 16-byte pieces. A CTA takes 8 KB of a sequence's; the first writes its table
+// row too. Bound by its chain (parent, its length and page, rows) and its launch:
+// 512 sequences with 44 rows of 656 bytes (30 MB moved) 8 us, 0.55 of the measured
+// copy rate.
 constexpr int kCopyPieces = 4;  // 16 bytes each, a thread's
 constexpr int kCopyBytes = kThreads * kCopyPieces * 16;
 

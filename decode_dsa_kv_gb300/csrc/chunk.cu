@@ -29,9 +29,16 @@
 // the products and their issue); 32 single tokens x 128 heads over 32,768
 // positions each 280 us, 4.3 TB/s (only the K stages come from HBM, and the ring
 // does not reach over the V stages between them); one token x 16 heads over 4096
-// positions 19 us (latency: plan, first loads, softmax, epilogue, merge). A row
+// positions 14.6 us (latency: plan, first loads, softmax, epilogue, merge). A row
 // tile of one key tile more costs a pair 6 us, a key tile more in the row tile it
 // has 2 to 4: a row tile is drained before the next one's scores begin.
+//
+// Trees: 16 of 64 nodes x 128 heads over 8192 positions each 1510 us, 0.79 of the
+// measured burst rate (1416 us, 0.84, as one launch), where the masks cost
+// nothing that shows (the same products without them, by stretches: 1720); 4 ragged
+// ones of up to 61 nodes x 128 heads over up to 32,768 8-bit positions 633 us (0.54:
+// shared-memory bandwidth, below; as bf16 rows 463), 32 of up to 8 nodes x 64 heads
+// over up to 2048 60 us (8-bit; bf16 46), one of 16 x 16 over 4096 16.8 us.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -90,7 +97,7 @@ constexpr int kMaxPairs = 80;
 // take the row tiles in turn, whole ones, and only the last of them are cut. All
 // pairs are then in the same request or two, whose rows stay in L2, where
 // stretches of the line would have them in all requests at once (16 trees of 64
-// nodes x 128 heads over 8192, 151 MB of rows: FIGURES).
+// nodes x 128 heads over 8192, 151 MB of rows: 1740 us by stretches, 1510 so).
 constexpr int kMaxShared = 64, kSharedUnits = 64;
 struct Shared {
   Request r;

@@ -10,6 +10,14 @@
 // what it already has, its child, sent to every CTA, a cluster barrier. Weights
 // are whole multiples of 2^-60 (verify.cuh): the drawn token does not depend on
 // the split.
+//
+// Measured: 32 trees over 131,072 tokens, at most 4 drafts accepted, 22 us from L2,
+// some 4.3 a step, of which (clocks of a step with every request on its way) the
+// loads take 2000 to 3000, the sums 2000, waiting for the slowest CTA 1300, the sums'
+// scan 1200, the draw 1800, the child 400 and the second barrier 550. Two CTAs an
+// SM of 256 threads, eight a request: as requests end, the others' rows are spread
+// over more SMs (four of 512 threads: 34 us; 16 of 128: 24.5 where this took 26.8,
+// but clusters above 8 are not portable). One greedy tree over 32,000: 6.2 us.
 #include <algorithm>
 
 #include "verify.cuh"
