@@ -100,10 +100,11 @@ template <int kFmt, bool kPairs>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ Args a) {
   const int lane = threadIdx.x & 31;
   const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);  // (below 2^32)
-  const int row = static_cast<int>(item / uint32_t(a.shares));
-  const int share = static_cast<int>(item - uint32_t(row) * a.shares);
+  const uint32_t number = item / uint32_t(a.shares);
+  const int share = static_cast<int>(item - number * a.shares);
   wait_previous_kernel();
-  if (row >= a.n) return;
+  if (number >= uint32_t(a.n)) return;
+  const int row = static_cast<int>(number);
   const int pos = a.pos[row];
   if (share > 0) {
     const int head0 = (share - 1) * kHeads + (lane >> 3), c = lane & 7;

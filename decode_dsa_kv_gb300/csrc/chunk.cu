@@ -253,13 +253,9 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
       for (int p = tid; p < a.pairs; p += threads)
         fits = fits && load[p] < stretch_of(total, a.pairs, p).count;
       if (__syncthreads_and(fits)) {
-        int64_t mine_load = 0, all_load;
-        if (tid < a.pairs) mine_load = load[tid];
-        scan(mine_load, &all_load);
-        int64_t before = 0;  // of the pairs before this one
-        for (int p = 0; p < pair; ++p) before += load[p];
-        from = all_load + (st.from - before);
-        count = st.count - load[pair];
+        const Stretch rest = stretch_behind(total, a.pairs, pair, load);
+        from = rest.from;
+        count = rest.count;
         if (tid == 0) bars->rounds = rounds;
       }
       __syncthreads();
@@ -286,38 +282,6 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
   }
   __syncthreads();
 }
-
-// A pair's row tiles and key tiles: of a tree, first its whole row tiles.
-template <bool kTree>
-struct Walker {
-  Walk walk;
-  int rounds, pairs, b, j;
-  __device__ __forceinline__ Walker(const Args& a, const Bars* bars, int pair)
-      : walk{bars->start_b, bars->start_j, bars->start_u, bars->count},
-        rounds(kTree ? bars->rounds : 0),
-        pairs(a.pairs),
-        b(0),
-        j(pair) {}
-  __device__ __forceinline__ bool next(const Args& a, Segment& s) {
-    if (!kTree || rounds == 0) return walk.next(a, s);
-    --rounds;
-    for (;; ++b) {  // (there are that many row tiles)
-      s.r = request(a, b);
-      const int tiles = row_tiles(a.H, s.r);
-      if (j < tiles) break;
-      j -= tiles;
-    }
-    s.b = b;
-    s.row0 = j * kRows;
-    s.rows = static_cast<int>(least(int64_t(kRows), int64_t(s.r.n) * a.H - s.row0));
-    s.end = s.r.ctx;
-    s.t0 = 0;
-    s.t1 = key_tiles(s.end);
-    s.starts = s.ends = true;
-    j += pairs;
-    return true;
-  }
-};
 
 // Reports lengths out of range (once per launch).
 __device__ __forceinline__ void check_lengths(const Args& a) {
@@ -902,7 +866,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
     return Loader{a, maps, bars, q_tile, ring, raw, rank, dsmem_addr(&bars->q_full, 0),
                   dsmem_addr(&bars->full[0], 0), lane, elect_one(), abort, k_step, min(4, k_step)};
   };
-  Walker<kTree> walk(a, bars, pair);
+  Walker<kTree> walk{{bars->start_b, bars->start_j, bars->start_u, bars->count},
+                     kTree ? bars->rounds : 0, a.pairs, 0, pair};
   Segment sg;
   if (warp < kSoftmaxWarps) {
     // ---------------- softmax and epilogue: kParts threads per TMEM lane ----------------
@@ -1323,7 +1288,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kFewBlocks)
   constexpr int kAhead = 8;
   wait_previous_kernel();
   const int lane = threadIdx.x & 31;
-  const int at = blockIdx.x * kMergeWarps + (threadIdx.x >> 5), n = at >> 2;  // this warp's row
+  const int at = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
   // slot 1 of every pair (a row tile's head) and slot 0 (the tail of one)
   int4 head[kRecords], tail[kRecords];
 #pragma unroll
@@ -1335,86 +1300,93 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kFewBlocks)
       tail[k] = a.meta[p * 2];
     }
   }
-  int pair = -1, first = 0, from = 0, rows = 0;
+  int rows = 0, upto[kRecords];  // rows of the line up to and with a pair's
   uint32_t ends[kRecords];
 #pragma unroll
   for (int k = 0; k < kRecords; ++k) {
-    const int mine = head[k].x >= 0 ? head[k].y : 0;
-    const int upto = rows + warp_inclusive_scan(mine);
-    const uint32_t past = __ballot_sync(0xffffffffu, upto > n);
-    if (past && pair < 0) {
-      const int who = __ffs(past) - 1;
-      pair = 32 * k + who;
-      first = __shfl_sync(0xffffffffu, head[k].x, who);
-      from = __shfl_sync(0xffffffffu, upto - mine, who);
-    }
-    rows = __shfl_sync(0xffffffffu, upto, 31);
+    if (head[k].x < 0) head[k].y = 0;
+    upto[k] = rows + warp_inclusive_scan(head[k].y);
+    rows = __shfl_sync(0xffffffffu, upto[k], 31);
     ends[k] = __ballot_sync(0xffffffffu, tail[k].x >= 0 && (tail[k].z & kEnds));
   }
-  if (pair < 0) return;
-  int parts = 0;
-#pragma unroll
-  for (int k = 0; k < kRecords; ++k) {
-    // (the pairs after this one)
-    const int skip = pair + 1 - 32 * k;
-    const uint32_t later = skip >= 32 ? 0u : skip <= 0 ? ends[k] : ends[k] >> skip << skip;
-    if (later && !parts) parts = 32 * k + __ffs(later) - pair;
-  }
-  const int r = n - from, col = (at & 3) * 32 + lane;
-  auto row_of = [&](int i) -> int64_t {
-    return int64_t(i == 0 ? pair * 2 + 1 : (pair + i) * 2) * a.part_rows + r;
-  };
-  auto load = [&](int i) {
-    return __ldcs(reinterpret_cast<const float4*>(a.opart + row_of(i) * DSA_DV) + col);
-  };
-  float4 ahead[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (i < parts) ahead[i] = load(i);
-  float2 stat = make_float2(-INFINITY, 0.f);
-  if (lane < parts) stat = a.ml[row_of(lane)];
-  float mx = stat.x;
+  // (once for a warp, unless requests share tokens that they may not)
 #pragma unroll 1
-  for (int i = lane + 32; i < parts; i += 32) mx = fmaxf(mx, a.ml[row_of(i)].x);
+  for (int n = at >> 2; n < rows; n += gridDim.x * (kMergeWarps / 4)) {
+    int pair = -1, first = 0, from = 0;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-  const float base = mx == -INFINITY ? 0.f : mx;
-  float sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float w, const float4& x) {
-    acc.x += w * x.x;
-    acc.y += w * x.y;
-    acc.z += w * x.z;
-    acc.w += w * x.w;
-  };
-#pragma unroll 1
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    if (i0) stat = i0 + lane < parts ? a.ml[row_of(i0 + lane)] : make_float2(-INFINITY, 0.f);
-    const float w = exp2f(stat.x - base);
-    sum += w * stat.y;
-    const int m = min(parts - i0, 32);
-    int i = 0;
-    if (i0 == 0) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        if (k < m) add(wk, ahead[k]);
+    for (int k = 0; k < kRecords; ++k) {
+      const uint32_t past = __ballot_sync(0xffffffffu, upto[k] > n);
+      if (past && pair < 0) {
+        const int who = __ffs(past) - 1;
+        pair = 32 * k + who;
+        first = __shfl_sync(0xffffffffu, head[k].x, who);
+        from = __shfl_sync(0xffffffffu, upto[k] - head[k].y, who);
       }
-      i = min(m, kAhead);
     }
-#pragma unroll 8
-    for (; i < m; ++i) add(__shfl_sync(0xffffffffu, w, i), load(i0 + i));
-  }
+    int parts = 0;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t row = int64_t(first) + r;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  reinterpret_cast<uint2*>(a.out + row * DSA_DV)[col] = make_uint2(
-      *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  if (lane == 0 && (at & 3) == 0 && a.lse)
-    a.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    for (int k = 0; k < kRecords; ++k) {
+      // (the pairs after this one)
+      const int skip = pair + 1 - 32 * k;
+      const uint32_t later = skip >= 32 ? 0u : skip <= 0 ? ends[k] : ends[k] >> skip << skip;
+      if (later && !parts) parts = 32 * k + __ffs(later) - pair;
+    }
+    const int r = n - from, col = (at & 3) * 32 + lane;
+    auto row_of = [&](int i) -> int64_t {
+      return int64_t(i == 0 ? pair * 2 + 1 : (pair + i) * 2) * a.part_rows + r;
+    };
+    auto load = [&](int i) {
+      return __ldcs(reinterpret_cast<const float4*>(a.opart + row_of(i) * DSA_DV) + col);
+    };
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < parts) ahead[i] = load(i);
+    float2 stat = make_float2(-INFINITY, 0.f);
+    if (lane < parts) stat = a.ml[row_of(lane)];
+    float mx = stat.x;
+#pragma unroll 1
+    for (int i = lane + 32; i < parts; i += 32) mx = fmaxf(mx, a.ml[row_of(i)].x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float w, const float4& x) {
+      acc.x += w * x.x;
+      acc.y += w * x.y;
+      acc.z += w * x.z;
+      acc.w += w * x.w;
+    };
+#pragma unroll 1
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      if (i0) stat = i0 + lane < parts ? a.ml[row_of(i0 + lane)] : make_float2(-INFINITY, 0.f);
+      const float w = exp2f(stat.x - base);
+      sum += w * stat.y;
+      const int m = min(parts - i0, 32);
+      int i = 0;
+      if (i0 == 0) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, k);
+          if (k < m) add(wk, ahead[k]);
+        }
+        i = min(m, kAhead);
+      }
+#pragma unroll 8
+      for (; i < m; ++i) add(__shfl_sync(0xffffffffu, w, i), load(i0 + i));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t row = int64_t(first) + r;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    reinterpret_cast<uint2*>(a.out + row * DSA_DV)[col] = make_uint2(
+        *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    if (lane == 0 && (at & 3) == 0 && a.lse)
+      a.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  }
 }
 
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -152,6 +152,50 @@ struct Walk {
   }
 };
 
+// What a pair takes behind rounds of whole row tiles, of which pair p has load[p]
+// units: an equal share of everything less its load (which has to be below it).
+PLAN_INLINE Stretch stretch_behind(int64_t total, int pairs, int pair, const int* load) {
+  const Stretch st = stretch_of(total, pairs, pair);
+  int64_t all = 0, before = 0;
+#ifdef __CUDACC__
+#pragma unroll 1
+#endif
+  for (int p = 0; p < pairs; ++p) {
+    if (p < pair) before += load[p];
+    all += load[p];
+  }
+  return {all + st.from - before, st.count - load[pair]};
+}
+
+// A pair's segments: of a tree, first `rounds` whole row tiles, every pairs-th
+// from row tile j of request b on (not causal: all of a request's row tiles have
+// all of its keys), then its stretch.
+template <bool kTree>
+struct Walker {
+  Walk walk;
+  int rounds, pairs, b, j;
+  template <class Args>
+  PLAN_INLINE bool next(const Args& a, Segment& s) {
+    if (!kTree || rounds == 0) return walk.next(a, s);
+    --rounds;
+    for (;; ++b) {  // (there are that many row tiles)
+      s.r = request(a, b);
+      const int tiles = row_tiles(a.H, s.r);
+      if (j < tiles) break;
+      j -= tiles;
+    }
+    s.b = b;
+    s.row0 = j * kRows;
+    s.rows = static_cast<int>(least(int64_t(kRows), int64_t(s.r.n) * a.H - s.row0));
+    s.end = s.r.ctx;
+    s.t0 = 0;
+    s.t1 = key_tiles(s.end);
+    s.starts = s.ends = true;
+    j += pairs;
+    return true;
+  }
+};
+
 // 64-key groups of key tile t that hold keys below `end`.
 PLAN_INLINE int groups(int end, int t) {
   return least(4, most(0, (end - t * kKeys + 63) >> 6));

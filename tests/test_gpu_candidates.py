@@ -892,3 +892,21 @@ def test_rows_past_32_bit_offsets(d, fmt):
     for i in range(5):
         assert np.array_equal(got[i, :split], want[i][:split])
     assert not got[5].any()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_request_behind_ones_that_share_tokens_is_attended_to_in_full(d, fmt):
+    # two requests over the same tokens (reported) have more rows to merge than the
+    # call has; the rows of the request behind them are merged all the same
+    c = Trees(d, fmt, 64, 16, [(30, 3000), (8, 2500)], seed=9, seen=lambda rng, n: np.tri(n, dtype=bool))
+    want, lse = c.run()
+    c.check(want, lse, every=11)
+    table, ctx = c.table, c.ctx
+    four = torch.cat([table[:1], table[:1], table[:1], table[1:]]).contiguous()
+    lens = torch.cat([ctx[:1], ctx[:1], ctx[:1], ctx[1:]]).contiguous()
+    cu = i32([0, 30, 0, 30, 38])
+    for tree in (None, c.mask):
+        out, z = c.kv.attend(c.q, cu, four, lens, tree=tree)
+        assert c.kv.synchronize() == d._abi.TS_DEVERR_ORDER
+        assert torch.allclose(out[30:].float(), want[30:].float(), rtol=2.0 ** -6, atol=2.0 ** -6)
+        assert torch.allclose(z[30:], lse[30:], rtol=0, atol=1e-4)
