@@ -1,5 +1,6 @@
-"""ctypes binding of libdsakv.so: the same entry points as include/dsakv.h,
-with argument marshalling only (tensors -> device pointers, streams -> handles).
+"""Binding of libdsakv.so (ctypes, the paged cache's calls in C++): the same entry
+points as include/dsakv.h, with argument marshalling only (tensors -> device
+pointers, streams -> handles).
 Every step of the path runs in the library's CUDA kernels; nothing here
 computes. Importing this module fails loudly when the library is missing."""
 from __future__ import annotations
@@ -328,91 +329,24 @@ def dsa_cache_row_bytes(fmt: int) -> int:
     return int(_lib.dsa_cache_row_bytes(fmt))
 
 
-def dsa_cache_write(latent, latent_stride, rope, rope_stride, slots, n, cache, num_slots, fmt,
-                    err=None, stream=None) -> int:
-    return _lib.dsa_cache_write(ptr(latent), latent_stride, ptr(rope), rope_stride, ptr(slots), n,
-                                ptr(cache), num_slots, fmt, ptr(err), stream_handle(stream))
+# The paged cache's calls: the same, marshalled in C++ (csrc/binding.cpp), since
+# theirs is what bounds the smallest of them.
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError(f"{_HERE}/_binding.so is missing: build it with "
+                      "`python -m decode_dsa_kv_gb300.build`") from e
 
-
-def dsa_cache_read(cache, num_slots, fmt, block_table, table_stride, page_size, pos, ctx_len, B, k,
-                   sel, err=None, stream=None) -> int:
-    return _lib.dsa_cache_read(ptr(cache), num_slots, fmt, ptr(block_table), table_stride,
-                               page_size, ptr(pos), ptr(ctx_len), B, k, ptr(sel), ptr(err),
-                               stream_handle(stream))
-
-
-def sfa_chunk_workspace_size(T: int, B: int, H: int) -> int:
-    return int(_lib.sfa_chunk_workspace_size(T, B, H))
-
-
-def sfa_mla_chunk(q, q_stride, cu_q, T, B, H, cache, num_slots, fmt, block_table, table_stride,
-                  page_size, ctx_len, causal, scale, out, lse, ws, ws_bytes, err=None,
-                  stream=None) -> int:
-    return _lib.sfa_mla_chunk(ptr(q), q_stride, ptr(cu_q), T, B, H, ptr(cache), num_slots, fmt,
-                              ptr(block_table), table_stride, page_size, ptr(ctx_len), int(causal),
-                              float(scale), ptr(out), ptr(lse), ptr(ws), ws_bytes, ptr(err),
-                              stream_handle(stream))
-
-
-def ts_verify_drafts(drafts, n_draft, target, target_stride, draft, draft_stride, u, B, n, V,
-                     tokens, accepted, err=None, stream=None) -> int:
-    return _lib.ts_verify_drafts(ptr(drafts), ptr(n_draft), ptr(target), target_stride, ptr(draft),
-                                 draft_stride, ptr(u), B, n, V, ptr(tokens), ptr(accepted),
-                                 ptr(err), stream_handle(stream))
-
-
-def dsa_tree_plan(parent, cu_q, T, B, ctx_len, block_table, table_stride, page_size, num_slots,
-                  pos, slots, mask, words, err=None, stream=None) -> int:
-    return _lib.dsa_tree_plan(ptr(parent), ptr(cu_q), T, B, ptr(ctx_len), ptr(block_table),
-                              table_stride, page_size, num_slots, ptr(pos), ptr(slots), ptr(mask),
-                              words, ptr(err), stream_handle(stream))
-
-
-def dsa_cache_append(latent, latent_stride, rope, rope_stride, pos, slots, n, freq, pairs, cache,
-                     num_slots, fmt, q_rope, q_rope_stride, q_rope_head, H, q, q_stride, err=None,
-                     stream=None) -> int:
-    return _lib.dsa_cache_append(ptr(latent), latent_stride, ptr(rope), rope_stride, ptr(pos),
-                                 ptr(slots), n, ptr(freq), int(pairs), ptr(cache), num_slots, fmt,
-                                 ptr(q_rope), q_rope_stride, q_rope_head, H, ptr(q), q_stride,
-                                 ptr(err), stream_handle(stream))
-
-
-def sfa_mla_tree(q, q_stride, cu_q, T, B, H, cache, num_slots, fmt, block_table, table_stride,
-                 page_size, ctx_len, mask, words, scale, out, lse, ws, ws_bytes, err=None,
-                 stream=None) -> int:
-    return _lib.sfa_mla_tree(ptr(q), q_stride, ptr(cu_q), T, B, H, ptr(cache), num_slots, fmt,
-                             ptr(block_table), table_stride, page_size, ptr(ctx_len), ptr(mask),
-                             words, float(scale), ptr(out), ptr(lse), ptr(ws), ws_bytes, ptr(err),
-                             stream_handle(stream))
-
-
-def ts_verify_tree(tokens, parent, cu_q, T, B, target, target_stride, u, V, depth, path, next,
-                   accepted, err=None, stream=None) -> int:
-    return _lib.ts_verify_tree(ptr(tokens), ptr(parent), ptr(cu_q), T, B, ptr(target),
-                               target_stride, ptr(u), V, depth, ptr(path), ptr(next),
-                               ptr(accepted), ptr(err), stream_handle(stream))
-
-
-def dsa_cache_keep(cache, num_slots, fmt, block_table, table_stride, page_size, cu_q, T, ctx_len, B,
-                   path, depth, accepted, new_len=None, err=None, stream=None) -> int:
-    return _lib.dsa_cache_keep(ptr(cache), num_slots, fmt, ptr(block_table), table_stride,
-                               page_size, ptr(cu_q), T, ptr(ctx_len), B, ptr(path), depth,
-                               ptr(accepted), ptr(new_len), ptr(err), stream_handle(stream))
-
-
-def ts_beam_workspace_size(B: int, K: int, V: int, n: int) -> int:
-    return int(_lib.ts_beam_workspace_size(B, K, V, n))
-
-
-def ts_beam_select(logits, dtype, row_stride, cum, B, K, V, n, tokens, parents, scores, ws,
-                   ws_bytes, err=None, stream=None) -> int:
-    return _lib.ts_beam_select(ptr(logits), dtype, row_stride, ptr(cum), B, K, V, n, ptr(tokens),
-                               ptr(parents), ptr(scores), ptr(ws), ws_bytes, ptr(err),
-                               stream_handle(stream))
-
-
-def dsa_cache_fork(cache, num_slots, fmt, block_table, table_stride, page_size, ctx_len, parents,
-                   spare, B, K, n, new_table=None, new_len=None, err=None, stream=None) -> int:
-    return _lib.dsa_cache_fork(ptr(cache), num_slots, fmt, ptr(block_table), table_stride,
-                               page_size, ptr(ctx_len), ptr(parents), ptr(spare), B, K, n,
-                               ptr(new_table), ptr(new_len), ptr(err), stream_handle(stream))
+dsa_cache_write = _binding.dsa_cache_write
+dsa_cache_read = _binding.dsa_cache_read
+sfa_chunk_workspace_size = _binding.sfa_chunk_workspace_size
+sfa_mla_chunk = _binding.sfa_mla_chunk
+ts_verify_drafts = _binding.ts_verify_drafts
+dsa_tree_plan = _binding.dsa_tree_plan
+dsa_cache_append = _binding.dsa_cache_append
+sfa_mla_tree = _binding.sfa_mla_tree
+ts_verify_tree = _binding.ts_verify_tree
+dsa_cache_keep = _binding.dsa_cache_keep
+ts_beam_workspace_size = _binding.ts_beam_workspace_size
+ts_beam_select = _binding.ts_beam_select
+dsa_cache_fork = _binding.dsa_cache_fork
