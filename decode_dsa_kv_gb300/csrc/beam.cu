@@ -520,10 +520,11 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
     e = __reduce_max_sync(0xffffffffu, e);
     top = __reduce_max_sync(0xffffffffu, top);
-    Beam beam = {e * kLn2, 0};
+    const double whole_m = e != INT_MIN ? e * kLn2 : -INFINITY;
+    const double wide_m = top ? double(from_order(top)) : -INFINITY;
+    Beam beam = {fmax(whole_m, wide_m), 0};
     double s = 0;
-    if (top == 0 || (e != INT_MIN && from_order(top) < 0.f)) {
-      // (a wide piece below the others adds nothing)
+    if (!(wide_m > whole_m - 200)) {  // (a wide part that far below adds nothing)
       uint64_t whole = 0;
       for (int i = lane; i < parts; i += 32) {
         const Piece p = piece(i);
@@ -534,7 +535,6 @@ __global__ void __launch_bounds__(kMergeThreads)
       for (int d = 16; d; d >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, d);
       s = static_cast<double>(whole) * 0x1p-30;
     } else {
-      beam.m = from_order(top);
       for (int i = lane; i < parts; i += 32) {
         const Piece p = piece(i);
         if (p.s > 0.f) s += p.s * exp(p.m() - beam.m);

@@ -609,6 +609,29 @@ def test_beam_select_of_odd_rows(d, dtype, kind, V, n):
             assert got[0][b].tolist() == want[0] and got[1][b].tolist() == want[1]
 
 
+@pytest.mark.parametrize("size", [2.0 ** 20, -2.0 ** 20])
+@pytest.mark.parametrize("first", [0, 1])
+def test_beam_select_where_the_sums_change_their_reference(d, size, first):
+    # values on both sides of the size from which a part of a row takes its largest
+    # value for reference, in parts of one row, a few apart
+    rng = np.random.default_rng(12)
+    V = 40000
+    x = np.empty((1, 2, V), dtype=np.float32)
+    near, far = size * (1 - 2.0 ** -18), size * (1 + 2.0 ** -19)     # 4 within, 2 past
+    x[0, :, :V // 2] = near if first else far
+    x[0, :, V // 2:] = far if first else near
+    x += rng.integers(-4, 5, x.shape).astype(np.float32) / 8
+    cum = np.array([[0.0, -0.5]], dtype=np.float32)
+    got = d.beam_select(torch.from_numpy(x).cuda(), torch.from_numpy(cum).cuda(), 20)
+    check_beams(x.astype(np.float64), cum, 20, got)
+    # the scores' differences from the logits are the sums' logarithms
+    for k in range(2):
+        mine = got[1][0] == k
+        t = got[0][0][mine].long().cpu().numpy()
+        want = oc.beam_scores(x[0], cum[0])[k, t]
+        assert np.all(np.abs(got[2][0][mine].double().cpu().numpy() - want) < 1e-5)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_beam_select_reports_nan_and_infinity(d, dtype):
     rng = np.random.default_rng(7)
