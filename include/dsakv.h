@@ -764,7 +764,7 @@ ts_status dsa_tree_plan(const int32_t* parent, const int32_t* cu_q, int T, int B
  * most |pos| 2^-54 of a turn, and then by its rounding to fp32. Sine and cosine
  * are fp32, the values round once to bf16. A row whose slot is negative, or past
  * the cache (TS_DEVERR_SLOT_RANGE), is skipped; its queries are turned all the
- * same. n = 0 enqueues nothing. */
+ * same. H <= 1024. n = 0 enqueues nothing. */
 ts_status dsa_cache_append(const void* latent, int64_t latent_stride, const void* rope,
                            int64_t rope_stride, const int32_t* pos, const int32_t* slots, int n,
                            const double* freq, int pairs, void* cache, int64_t num_slots, int fmt,

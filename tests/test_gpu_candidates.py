@@ -320,6 +320,24 @@ def test_tree_attention_of_chains_is_the_causal_one(d, fmt):
     assert torch.allclose(lse, l2, rtol=0, atol=1e-4)
 
 
+@pytest.mark.parametrize("H, reqs", [(16, [(9, 300), (40, 41), (1, 700)]), (128, [(100, 3300)] * 4)])
+def test_tree_attention_over_8_bit_rows_is_that_over_their_read_back(d, H, reqs):
+    c = Trees(d, "e4m3", 64, H, reqs, seed=6)
+    out, lse = c.run()
+    assert c.kv.synchronize() == 0
+    wide = d.PagedKV(c.kv.num_pages, 64, "bf16")
+    for b, (_, n) in enumerate(reqs):
+        pos = torch.arange(n, dtype=torch.int32, device="cuda").view(1, n)
+        rows = c.kv.read(c.table[b:b + 1], c.ctx[b:b + 1], pos)[0]
+        at = torch.arange(n, device="cuda")
+        slots = c.table[b].long()[at // 64] * 64 + at % 64
+        wide.write(rows[:, :512], rows[:, 512:], slots.to(torch.int32))
+    assert c.kv.synchronize() == 0
+    o2, l2 = wide.attend(c.q, c.cu, c.table, c.ctx, scale=1 / 24, tree=c.mask)
+    assert wide.synchronize() == 0
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
 def test_tree_attention_reports_more_nodes_than_bits(d):
     c = Trees(d, "bf16", 16, 16, [(40, 40), (3, 20)], seed=4, words=1)
     out, lse = c.run()
