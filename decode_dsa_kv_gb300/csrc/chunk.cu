@@ -98,9 +98,6 @@ constexpr int kMaxPairs = 80;
 // pairs are then in the same request or two, whose rows stay in L2, where
 // stretches of the line would have them in all requests at once (16 trees of 64
 // nodes x 128 heads over 8192, 151 MB of rows: 1740 us by stretches, 1510 so).
-// Not over 8-bit rows, whose kernel is bound by shared memory: 4 trees of up to
-// 61 x 128 over up to 32,768 635 us by stretches and 631 so, 1 x 1024 x 128 over 8192
-// 2100 and 2135 (the walk's registers).
 constexpr int kMaxShared = 64, kSharedUnits = 64;
 struct Shared {
   Request r;
@@ -191,7 +188,7 @@ __device__ __forceinline__ Request request(const Args& a, int b) {
 
 // The pair's stretch of the line of all units: thread-per-request sums, then
 // the request, row tile and key tile that the stretch begins in.
-template <bool kRounds>
+template <bool kTree>
 __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   auto units_of = [&](int b) -> int64_t {
@@ -225,7 +222,7 @@ __device__ __forceinline__ void plan(const Args& a, Bars* bars, int pair) {
   int64_t inc = scan(mine, &total);
   const Stretch st = stretch_of(total, a.pairs, pair);
   int64_t from = st.from, count = st.count;
-  if (kRounds) {
+  if (kTree) {
     if (tid == 0) bars->rounds = 0;
     if (a.B <= kMaxShared && total >= int64_t(kSharedUnits) * a.pairs && total < INT_MAX) {
       Shared s = {};
@@ -859,8 +856,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
   tc_fence_before();
   cluster_arrive();
   if (blockIdx.x == 0) check_lengths(a);
-  constexpr bool kRounds = kTree && !Lay::k8;
-  plan<kRounds>(a, bars, pair);
+  plan<kTree>(a, bars, pair);
   cluster_wait();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_slot;
@@ -870,8 +866,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<kFmt>::kThrea
     return Loader{a, maps, bars, q_tile, ring, raw, rank, dsmem_addr(&bars->q_full, 0),
                   dsmem_addr(&bars->full[0], 0), lane, elect_one(), abort, k_step, min(4, k_step)};
   };
-  Walker<kRounds> walk{{bars->start_b, bars->start_j, bars->start_u, bars->count},
-                       kRounds ? bars->rounds : 0, a.pairs, 0, pair};
+  Walker<kTree> walk{{bars->start_b, bars->start_j, bars->start_u, bars->count},
+                     kTree ? bars->rounds : 0, a.pairs, 0, pair};
   Segment sg;
   if (warp < kSoftmaxWarps) {
     // ---------------- softmax and epilogue: kParts threads per TMEM lane ----------------
