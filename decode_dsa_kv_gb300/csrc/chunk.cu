@@ -98,6 +98,10 @@ constexpr int kMaxPairs = 80;
 // pairs are then in the same request or two, whose rows stay in L2, where
 // stretches of the line would have them in all requests at once (16 trees of 64
 // nodes x 128 heads over 8192, 151 MB of rows: 1740 us by stretches, 1510 so).
+// 8-bit rows, whose kernel is bound by shared memory, gain nothing (4 trees of up to
+// 61 x 128 over up to 32,768: 635 and 631; 1 x 1024 x 128 over 8192: 2100 and 2135, the
+// walk's registers): they are shared out alike so that their results stay those of
+// the same rows in bf16, bit for bit.
 constexpr int kMaxShared = 64, kSharedUnits = 64;
 struct Shared {
   Request r;
