@@ -73,7 +73,7 @@ __device__ __forceinline__ uint64_t key_of(float x, int t) {
 }
 
 struct Piece {
-  float s;    // sum of exp(x - m)
+  float s;    // sum of exp(x - m), in [1, 2) unless m is a value (or s is 0)
   int e;      // m = e log 2, or
   float top;  // (where e is kWide) this
   __device__ __forceinline__ double m() const;
@@ -348,8 +348,15 @@ __global__ void __launch_bounds__(kThreads, 7)
     float s = y.x + y.y;
 #pragma unroll
     for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (lane == 0)
-      sums[int64_t(blockIdx.x) * kWarps + warp] = {s, wide ? kWide : static_cast<int>(e), ref};
+    // s is brought to [1, 2), its exponent goes to E (exact): E is that of the first
+    // rounds' values, and s above it may be as large as 2^77
+    int whole = static_cast<int>(e);
+    if (!wide && s >= 0x1p-126f) {
+      const uint32_t bits = __float_as_uint(s);
+      whole += static_cast<int>(bits >> 23) - 127;
+      s = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+    }
+    if (lane == 0) sums[int64_t(blockIdx.x) * kWarps + warp] = {s, wide ? kWide : whole, ref};
   }
 
   // ---- the n best ----
@@ -443,7 +450,7 @@ struct Candidate {
   }
 };
 
-// log s of s >= 2^-30, within 2^-29 (2^25 values tried): s = 2^k c (1 + r) with c a float of
+// log s of s >= 2^-44, within 2^-29 (2^25 values tried): s = 2^k c (1 + r) with c a float of
 // [1/sqrt 2, sqrt 2] and |r| below 2^-24, log c = 2 artanh(q), q = (c - 1) / (c +
 // 1), of which only q itself needs two floats. (CUDA's own of a double takes 1.2
 // us here, where fp64 is slow: a third of the kernel.)
@@ -479,6 +486,9 @@ struct Beam {
 // between those, the bound, the list and the places.
 constexpr int kMergeThreads = 256;
 constexpr int kAhead = 4;  // candidates a thread holds in registers
+// A row has at most 2^18 parts below 2 (2^30 values in pieces of 2^14, four warps a
+// piece): their sum stays below 2^64, and what each loses adds up to less than 2^-26.
+constexpr int kShift = 44;
 __global__ void __launch_bounds__(kMergeThreads)
     beam_merge_kernel(const uint64_t* best, const Piece* sums, const float* cum, int K, int V,
                       int n, int pieces, Beam* beams, int32_t* tokens, int32_t* parents,
@@ -501,8 +511,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     ahead[j] = i < all ? best[i] : 0;
   }
   if (tid == 0) listed = 0;
-  // every beam's sum of exponentials, in whole multiples of 2^-30 of 2^e: a warp
-  // a beam
+  // every beam's sum of exponentials, in whole multiples of 2^-kShift of 2^e, e the
+  // largest of its parts' (each below 2): a warp a beam
   beams += int64_t(b) * K;
   for (int k = warp; k < K; k += kMergeThreads / 32) {
     const int parts = pieces * kWarps;
@@ -529,11 +539,11 @@ __global__ void __launch_bounds__(kMergeThreads)
       for (int i = lane; i < parts; i += 32) {
         const Piece p = piece(i);
         if (p.s > 0.f && p.e != kWide)
-          whole += __float2ull_rn(ldexpf(p.s, max(p.e - e, -100) + 30));
+          whole += __float2ull_rn(ldexpf(p.s, max(p.e - e, -100) + kShift));
       }
 #pragma unroll
       for (int d = 16; d; d >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, d);
-      s = static_cast<double>(whole) * 0x1p-30;
+      s = static_cast<double>(whole) * (1.0 / (uint64_t(1) << kShift));
     } else {
       for (int i = lane; i < parts; i += 32) {
         const Piece p = piece(i);
