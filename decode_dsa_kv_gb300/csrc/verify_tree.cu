@@ -223,6 +223,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_tree_kernel(const __grid_c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int warps = a.cluster * kWarps, me = rank * kWarps + warp;
   launch_dependents();
+  // Another CTA's shared memory may be written only once that CTA has started: every
+  // CTA arrives here, and waits for the others behind the first row's loads.
+  cluster_arrive_relaxed();
+  bool started = false;
   const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1);
   const int q0 = min(max(c0, 0), a.T), n = max(min(c1, a.T) - q0, 0);
   int32_t* path = a.path + int64_t(b) * (a.depth + 1);
@@ -262,6 +266,11 @@ __global__ void __launch_bounds__(kThreads, 2) verify_tree_kernel(const __grid_c
     for (int r = 0; r < a.rounds; ++r) {
       const int first = (r * warps + me) * kHeld;
       row.load(v, first, a.u ? 0.f : -INFINITY);
+      if (!started) {
+        __syncwarp();
+        cluster_wait();
+        started = true;
+      }
       if (a.u) {
         sums_of(v, upto, &bad);
         if (lane < a.cluster)
@@ -380,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_tree_kernel(const __grid_c
   }
   // (greedy: the last step's parts may still be on their way to a CTA)
   __syncwarp();
+  if (!started) cluster_wait();  // (a request without a node)
   cluster_sync_all();
 }
 
