@@ -5,8 +5,8 @@
 //
 // Arguments by the C type: a pointer is None, an address or anything with
 // data_ptr(); a stream None (the current one), a handle or anything with
-// cuda_stream; numbers and truth values as they are. Those after the required
-// ones default to None.
+// cuda_stream; whole numbers as they are, flags what int() takes, a scale what
+// float() takes. Those after the required ones default to None.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -88,9 +88,11 @@ bool get(PyObject* o, T* out) {
     *out = reinterpret_cast<T>(v);
     return true;
   } else if constexpr (std::is_floating_point_v<T>) {
-    const double v = PyFloat_AsDouble(o);
-    *out = static_cast<T>(v);
-    return !(v == -1.0 && PyErr_Occurred());
+    PyObject* x = PyNumber_Float(o);
+    if (!x) return false;
+    *out = static_cast<T>(PyFloat_AS_DOUBLE(x));
+    Py_DECREF(x);
+    return true;
   } else {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) return false;
@@ -120,16 +122,18 @@ struct Signature<R (*)(A...)> {
   }
 };
 
-// A function, its parameters' names and how many of them have no default.
+// A function, its parameters' names, which of them are flags and how many have no
+// default.
 struct Names {
   PyObject* name[32];
+  uint32_t flags;
   Py_ssize_t required;
 };
 
 template <auto* kFunction>
 struct Entry {
   using S = Signature<decltype(kFunction)>;
-  static_assert(S::kCount <= 32, "names");
+  static_assert(S::kCount < 32, "names");
   static Names names;
   static PyObject* run(PyObject*, PyObject* const* args, Py_ssize_t given, PyObject* keywords) {
     PyObject* o[32];
@@ -156,25 +160,38 @@ struct Entry {
         PyErr_Format(PyExc_TypeError, "argument %R is missing", names.name[i]);
         return nullptr;
       }
+    for (Py_ssize_t i = 0; names.flags >> i; ++i) {
+      if (!(names.flags >> i & 1) || PyLong_Check(o[i])) continue;
+      PyObject* x = PyNumber_Long(o[i]);
+      if (!x) return nullptr;
+      o[i] = PyObject_IsTrue(x) ? Py_True : Py_False;
+      Py_DECREF(x);
+    }
     return S::call(kFunction, o, std::make_index_sequence<S::kCount>());
   }
 };
 template <auto* kFunction>
 Names Entry<kFunction>::names;
 
-// Fills in the names ("a b c | err stream": those after the bar have defaults).
+// Fills in the names ("a b ?c | err stream": c is a flag, those after the bar have
+// defaults).
 template <auto* kFunction>
 bool name(const char* list) {
   Names& n = Entry<kFunction>::names;
   Py_ssize_t count = 0;
   n.required = -1;
+  n.flags = 0;
   for (const char* p = list; *p;) {
     const char* end = p;
     while (*end && *end != ' ') ++end;
     if (*p == '|') {
       n.required = count;
     } else {
-      if (count == 32) return false;
+      if (count == 31) return false;
+      if (*p == '?') {
+        n.flags |= 1u << count;
+        ++p;
+      }
       n.name[count] = PyUnicode_FromStringAndSize(p, end - p);
       if (!n.name[count]) return false;
       PyUnicode_InternInPlace(&n.name[count++]);
@@ -216,12 +233,12 @@ PyMODINIT_FUNC PyInit__binding() {
                             "sel | err stream") &&
       name<&sfa_chunk_workspace_size>("T B H") &&
       name<&sfa_mla_chunk>("q q_stride cu_q T B H cache num_slots fmt block_table table_stride "
-                           "page_size ctx_len causal scale out lse ws ws_bytes | err stream") &&
+                           "page_size ctx_len ?causal scale out lse ws ws_bytes | err stream") &&
       name<&ts_verify_drafts>("drafts n_draft target target_stride draft draft_stride u B n V "
                               "tokens accepted | err stream") &&
       name<&dsa_tree_plan>("parent cu_q T B ctx_len block_table table_stride page_size num_slots "
                            "pos slots mask words | err stream") &&
-      name<&dsa_cache_append>("latent latent_stride rope rope_stride pos slots n freq pairs cache "
+      name<&dsa_cache_append>("latent latent_stride rope rope_stride pos slots n freq ?pairs cache "
                               "num_slots fmt q_rope q_rope_stride q_rope_head H q q_stride | err "
                               "stream") &&
       name<&sfa_mla_tree>("q q_stride cu_q T B H cache num_slots fmt block_table table_stride "
