@@ -19,15 +19,16 @@ struct Turns {
 // at most 1), the product with pos is exact, so an angle is off by pos times
 // that, and no range reduction of a large angle is needed (a double angle of
 // position 10^6 is off by 2^-34, and its fp64 arithmetic takes 16 clocks an
-// instruction here). Lane i computes pair i, the lanes that hold its values
-// fetch it.
+// instruction here). A freq that is infinite or no number gives no number. Lane i
+// computes pair i, the lanes that hold its values fetch it.
 template <bool kPairs>
 __device__ __forceinline__ Turns turns_of(const double* freq, int pos, int lane) {
-  const double turn = freq[lane] * 0.15915494309189533577;  // 1 / 2 pi
+  const double f = freq[lane], turn = f * 0.15915494309189533577;  // 1 / 2 pi
   const uint64_t step = static_cast<uint64_t>(__double2ull_rz((turn - floor(turn)) * 0x1p64));
   const int64_t at = static_cast<int64_t>(step * static_cast<uint64_t>(int64_t(pos)));
+  const float none = (__double2hiint(f) & 0x7ff00000) == 0x7ff00000 ? NAN : 0.f;
   float s, c;
-  sincospif(static_cast<float>(static_cast<int32_t>(at >> 32)) * 0x1p-31f, &s, &c);
+  sincospif(static_cast<float>(static_cast<int32_t>(at >> 32)) * 0x1p-31f + none, &s, &c);
   Turns t;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {

@@ -753,7 +753,8 @@ ts_status dsa_tree_plan(const int32_t* parent, const int32_t* cu_q, int T, int B
  *   (a, b) -> (a cos - b sin, a sin + b cos)
  *   latent, rope, slots, n, cache   as dsa_cache_write's
  *   pos    int32 [n]                any value
- *   freq   double [32]              radians a position (device memory)
+ *   freq   double [32]              radians a position (device memory); an infinite
+ *                                   one, or a NaN, turns its pair's values to NaN
  *   q_rope bf16 [n][H][64]          the queries' rope parts before the rotation,
  *                                   tokens q_rope_stride and heads q_rope_head values apart
  *                                   (>= 64, multiples of 8; 16-byte aligned), or NULL: no
