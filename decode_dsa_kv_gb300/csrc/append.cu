@@ -28,7 +28,7 @@ __device__ __forceinline__ Turns turns_of(const double* freq, int pos, int lane)
   const int64_t at = static_cast<int64_t>(step * static_cast<uint64_t>(int64_t(pos)));
   const float none = (__double2hiint(f) & 0x7ff00000) == 0x7ff00000 ? NAN : 0.f;
   float s, c;
-  sincospif(static_cast<float>(static_cast<int32_t>(at >> 32)) * 0x1p-31f + none, &s, &c);
+  sincospif(static_cast<float>(at) * 0x1p-63f + none, &s, &c);  // (rounded once, of its size)
   Turns t;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {

@@ -762,8 +762,8 @@ ts_status dsa_tree_plan(const int32_t* parent, const int32_t* cu_q, int T, int B
  *   q      bf16 [n][H][576]         its values 512..575 are written, tokens q_stride apart
  *                                   (>= H * 576, a multiple of 8; 16-byte aligned)
  * The angle is reduced in whole 2^-64 turns: for |freq| <= 1 it is off by at
- * most |pos| 2^-54 of a turn, and then by its rounding to fp32. Sine and cosine
- * are fp32, the values round once to bf16. A row whose slot is negative, or past
+ * most |pos| 2^-54 of a turn, and then by its rounding to fp32, 2^-24 of its size
+ * (at most half a turn). Sine and cosine are fp32, the values round once to bf16. A row whose slot is negative, or past
  * the cache (TS_DEVERR_SLOT_RANGE), is skipped; its queries are turned all the
  * same. H <= 1024. n = 0 enqueues nothing. */
 ts_status dsa_cache_append(const void* latent, int64_t latent_stride, const void* rope,

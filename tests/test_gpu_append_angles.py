@@ -1,5 +1,5 @@
 """Appended rows and queries at the ends of the angles' range: frequencies that
-are no numbers."""
+are no numbers, and ones so small that an angle is a tiny part of a turn."""
 import math
 
 import numpy as np
@@ -48,3 +48,25 @@ def test_a_frequency_that_is_no_number_gives_none(d, interleaved):
     hit = np.isin(pair, [3, 17, 31])
     assert np.all(np.isnan(got[:, hit]))
     assert np.array_equal(got[:, ~hit], want[:, ~hit])
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_small_angles(d, interleaved, sign):
+    # a = 1, b = 0: the turned pair is (cos, sin) itself
+    freq = sign * 10.0 ** -np.linspace(3, 10, 32)
+    pos = [1, 2, 3, 50, 1000, 4097, 65535]
+    one = torch.zeros((len(pos), 64), dtype=torch.bfloat16, device="cuda")
+    if interleaved:
+        one[:, 0::2] = 1
+    else:
+        one[:, :32] = 1
+    got = appended(d, one, pos, freq, interleaved)
+    c, s = (got[:, 0::2], got[:, 1::2]) if interleaved else (got[:, :32], got[:, 32:])
+    angle = np.asarray(pos)[:, None] * freq
+    # the angle: |pos| 2^-54 of a turn, then 2^-24 of itself; its sine (2 units in
+    # the last place of fp32), and one rounding to bf16
+    for v, want in ((c, np.cos(angle)), (s, np.sin(angle))):
+        bound = (1.01 * BF16_HALF_STEP + 2.0 ** -21) * np.abs(want) + \
+            2 * math.pi * 2.0 ** -54 * np.asarray(pos)[:, None]
+        assert np.all(np.abs(v - want) <= bound), float((np.abs(v - want) / bound).max())
