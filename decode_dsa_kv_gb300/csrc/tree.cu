@@ -62,8 +62,22 @@ __global__ void __launch_bounds__(kPlanThreads)
   };
   if (b == B) {
     const int first = min(max(cu_q[0], 0), T), last = min(max(cu_q[B], 0), T);
-    for (int t = tid; t < first; t += kPlanThreads) none(t);
-    for (int64_t t = int64_t(last) + tid; t < T; t += kPlanThreads) none(static_cast<int>(t));
+    bool ascends = cu_q[0] >= 0 && cu_q[B] <= T;
+    for (int i = tid; i < B; i += kPlanThreads) ascends = ascends && cu_q[i] <= cu_q[i + 1];
+    if (__syncthreads_and(ascends)) {
+      for (int t = tid; t < first; t += kPlanThreads) none(t);
+      for (int64_t t = int64_t(last) + tid; t < T; t += kPlanThreads) none(static_cast<int>(t));
+      return;
+    }
+    // (reported; requests may then lie anywhere among the tokens: one by one)
+    for (int64_t t = tid; t < T; t += kPlanThreads) {
+      bool has = false;
+      for (int i = 0; i < B && !has; ++i) {
+        const int q0 = min(max(cu_q[i], 0), T);
+        has = t >= q0 && t < min(cu_q[i + 1], T);
+      }
+      if (!has) none(static_cast<int>(t));
+    }
     return;
   }
   const Request r = tree_of(cu_q, T, ctx_len, table.max_ctx, b, tid == 0, err);
