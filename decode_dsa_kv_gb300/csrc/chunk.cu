@@ -294,7 +294,11 @@ __device__ __forceinline__ void check_lengths(const Args& a) {
     const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1), ctx = __ldg(a.ctx_len + b);
     if (c0 < 0 || c1 < c0 || c1 > a.T) report(a.err, TS_DEVERR_ORDER);
     if (ctx < 0 || ctx > a.max_ctx) report(a.err, TS_DEVERR_CTX);
-    if (a.tree && int64_t(c1) - c0 > 32 * a.words) report(a.err, TS_DEVERR_COUNT);
+    if (a.tree) {
+      const Request r = request(a, b);
+      if (r.n > r.ctx) report(a.err, TS_DEVERR_CTX);
+      if (int64_t(c1) - c0 > 32 * a.words) report(a.err, TS_DEVERR_COUNT);
+    }
   }
 }
 

@@ -780,7 +780,8 @@ ts_status dsa_cache_append(const void* latent, int64_t latent_stride, const void
  *                           seen. dsa_tree_plan's, or any other; a node that
  *                           sees nothing has out = 0 and lse = -infinity.
  * Everything else, the workspace too, as sfa_mla_chunk. More nodes than 32 *
- * words set TS_DEVERR_COUNT. */
+ * words set TS_DEVERR_COUNT, more than ctx_len TS_DEVERR_CTX (the first ones then
+ * have no position, and no node sees them). */
 ts_status sfa_mla_tree(const void* q, int64_t q_stride, const int32_t* cu_q, int T, int B, int H,
                        const void* cache, int64_t num_slots, int fmt, const int32_t* block_table,
                        int64_t table_stride, int page_size, const int32_t* ctx_len,

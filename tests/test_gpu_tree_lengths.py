@@ -1,5 +1,5 @@
-"""Trees whose lengths are out of order: what is planned for the tokens that one
-request has, or none, and what is reported."""
+"""Trees whose lengths are out of order or do not fit their context: what is
+planned for the tokens that one request has, or none, and what is reported."""
 import numpy as np
 import pytest
 
@@ -7,7 +7,9 @@ torch = pytest.importorskip("torch")
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
 
-from test_gpu_paged import i32  # noqa: E402
+import oracle  # noqa: E402
+from test_gpu_candidates import FORMATS, Trees  # noqa: E402
+from test_gpu_paged import i32, output_bound  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -43,3 +45,21 @@ def test_tokens_of_one_request_or_none_where_lengths_are_out_of_order(d, cu, T):
     want = e.TS_DEVERR_ORDER if cu != sorted(cu) or cu[0] < 0 or cu[-1] > T else 0
     want |= e.TS_DEVERR_COUNT if max(count) > 1024 else 0
     assert kv.synchronize() == want
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_tree_attention_reports_more_nodes_than_positions(d, fmt):
+    c = Trees(d, fmt, 16, 16, [(5, 5), (7, 40), (9, 9)], seed=21)
+    want, _ = c.run()
+    c.check(*c.run())
+    # the first request's nodes 0 and 1, the last one's 0 to 8 have no position then
+    c.ctx.copy_(i32([3, 40, 0]))
+    out, lse = c.run()
+    assert c.kv.synchronize() == d._abi.TS_DEVERR_CTX
+    assert torch.equal(out[5:12], want[5:12])
+    assert torch.all(out[12:] == 0) and torch.all(torch.isneginf(lse[12:]))
+    for i in range(5):
+        K = c.K[0][:3][c.seen[0][i, 2:]]
+        o, z, mean_abs, size = oracle.chunk_attention(c.q64[i:i + 1], K, len(K), False, 1 / 24)
+        assert np.all(np.abs(out[i:i + 1].double().cpu().numpy() - o) <= output_bound(o, mean_abs, size))
+        assert np.array_equal(np.isneginf(z), torch.isneginf(lse[i:i + 1]).cpu().numpy())
