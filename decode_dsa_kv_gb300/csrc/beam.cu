@@ -723,7 +723,11 @@ __global__ void __launch_bounds__(kThreads) cache_fork_kernel(const __grid_const
       row[j] = j < last ? old[j] : j == last && p >= 0 ? a.spare[i] : -1;
     if (tid == 0) a.new_len[i] = ctx;
   }
-  if (rows == 0) return;  // (and a sequence that is none)
+  if (rows == 0) {  // (and a sequence that is none)
+    if (reports && p >= 0 && last < a.stride && (a.spare[i] < 0 || a.spare[i] >= a.pages))
+      report(a.err, TS_DEVERR_SLOT_RANGE);
+    return;
+  }
   const int64_t src = old[last], dst = a.spare[i];
   if (src < 0 || src >= a.pages || dst < 0 || dst >= a.pages) {
     if (reports) report(a.err, TS_DEVERR_SLOT_RANGE);

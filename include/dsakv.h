@@ -881,8 +881,9 @@ ts_status ts_beam_select(const void* logits, int dtype, int64_t row_stride, cons
  *   new_table   int32 [B * n][table_stride], new_len int32 [B * n]  out, other
  *               memory than the inputs'; both NULL: the rows alone, for the
  *               other layers' caches
- * A parent out of range sets TS_DEVERR_PARENT and counts as -1; a page outside
- * the cache sets TS_DEVERR_SLOT_RANGE, its rows are then not copied; a ctx_len
+ * A parent out of range sets TS_DEVERR_PARENT and counts as -1; a spare page or a
+ * partial last page outside the cache sets TS_DEVERR_SLOT_RANGE, no row is then
+ * copied (the tables get their entries all the same); a ctx_len
  * below 0 or past the table sets TS_DEVERR_CTX (taken as the nearest valid
  * value). A sequence that fills its table gets no spare page. B = 0 enqueues
  * nothing. */
