@@ -848,8 +848,10 @@ ts_status dsa_cache_keep(void* cache, int64_t num_slots, int fmt, const int32_t*
  * parent -1 and score -infinity. A finished sequence is carried on by a row
  * that is -infinity but for its padding token. A NaN or +infinity among the
  * logits or in cum sets TS_DEVERR_NAN and counts as -infinity. Scores are
- * compared in 64 bits, the sums of exponentials joined in 64 bits (each
- * exponential is fp32: the log within some 1e-7).
+ * compared in 64 bits. A log of a sum is off by less than 2^-17 (exponentials of
+ * 2^-22 and at most 71 additions in fp32, the parts then joined in 64 bits; of
+ * normal logits 5e-8 root mean square), 2^-20 where one token has nearly
+ * everything.
  *   ws      workspace of ts_beam_workspace_size(B, K, V, n) bytes, 256-byte
  *           aligned, contents need not be preserved; calls that may overlap on
  *           the GPU need one each
