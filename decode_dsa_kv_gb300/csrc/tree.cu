@@ -61,10 +61,11 @@ __global__ void __launch_bounds__(kPlanThreads)
       for (int k = 0; k < words; ++k) mask[int64_t(t) * words + k] = 0;
   };
   if (b == B) {
-    const int first = min(max(cu_q[0], 0), T), last = min(max(cu_q[B], 0), T);
-    bool ascends = cu_q[0] >= 0 && cu_q[B] <= T;
-    for (int i = tid; i < B; i += kPlanThreads) ascends = ascends && cu_q[i] <= cu_q[i + 1];
-    if (__syncthreads_and(ascends)) {
+    const int c0 = cu_q[0], c1 = cu_q[B];
+    int falls = c0 < 0 | c1 > T;
+    for (int i = tid; i < B; i += kPlanThreads) falls |= cu_q[i] > cu_q[i + 1];  // (all at once)
+    const int first = min(max(c0, 0), T), last = min(max(c1, 0), T);
+    if (!__syncthreads_or(falls)) {
       for (int t = tid; t < first; t += kPlanThreads) none(t);
       for (int64_t t = int64_t(last) + tid; t < T; t += kPlanThreads) none(static_cast<int>(t));
       return;
