@@ -26,9 +26,12 @@ __device__ __forceinline__ Turns turns_of(const double* freq, int pos, int lane)
   const double f = freq[lane], turn = f * 0.15915494309189533577;  // 1 / 2 pi
   const uint64_t step = static_cast<uint64_t>(__double2ull_rz((turn - floor(turn)) * 0x1p64));
   const int64_t at = static_cast<int64_t>(step * static_cast<uint64_t>(int64_t(pos)));
-  const float none = (__double2hiint(f) & 0x7ff00000) == 0x7ff00000 ? NAN : 0.f;
+  // to fp32 from both halves, the lower one signed (one instruction for 64 bits takes
+  // longer; a half turn's sign may change: the same angle)
+  const int lo = static_cast<int>(at), hi = static_cast<int>((at + 0x80000000ll) >> 32);
+  const float unit = (__double2hiint(f) & 0x7ff00000) == 0x7ff00000 ? NAN : 0x1p-31f;
   float s, c;
-  sincospif(static_cast<float>(at) * 0x1p-63f + none, &s, &c);  // (rounded once, of its size)
+  sincospif(fmaf(static_cast<float>(lo), 0x1p-32f, static_cast<float>(hi)) * unit, &s, &c);
   Turns t;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
