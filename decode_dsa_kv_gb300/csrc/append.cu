@@ -99,7 +99,7 @@ struct Args {
 // memory: 4095 tokens of 128 heads (144 MB, the queries' parts 128 bytes of every
 // 384 read and of every 1152 written) in 25.7 us, 0.83 of the measured copy rate;
 // with 8 heads a warp 27.9, with 32 27.1, in blocks of 256 threads 27.1. 991 nodes of
-// 32 trees, 8-bit rows, behind their plan: 7.8 us; one token of 16 heads 1.5.
+// 32 trees, 8-bit rows, behind their plan: 8.0 us; one token of 16 heads 1.6.
 template <int kFmt, bool kPairs>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ Args a) {
   const int lane = threadIdx.x & 31;

@@ -13,7 +13,11 @@
 // it reads; with the bound it reads again the few that reach it. The values
 // above the bound are listed in shared memory, and a value's place is the number
 // of larger ones. Where more reach the bound than the list holds (rows of equal
-// values, or sorted ones), the bound is raised by bisection until they fit.
+// values, or sorted ones), the bound is raised by bisection until they fit, at a
+// second reading of the piece a step: 64 x 8 beams over 131,072 bf16 logits of one
+// value 2.8 ms, of a type's lowest value but for five 6.2 ms, rising by 1e-3 1.4 ms,
+// where normal ones, a mask of the lowest value in nine of ten places or of
+// -infinity, and logits in whole quarters all take 37 us.
 //
 // A sum of exponentials is s e^m. For a warp m is E log 2 with E whole, and
 // exp(x - m) is taken as 2^(x log2(e) - E) with log2(e) in two floats: sums then

@@ -34,11 +34,12 @@
 // has 2 to 4: a row tile is drained before the next one's scores begin.
 //
 // Trees: 16 of 64 nodes x 128 heads over 8192 positions each 1510 us, 0.79 of the
-// measured burst rate (1416 us, 0.84, as one launch), where the masks cost
-// nothing that shows (the same products without them, by stretches: 1720); 4 ragged
-// ones of up to 61 nodes x 128 heads over up to 32,768 8-bit positions 633 us (0.54:
-// shared-memory bandwidth, below; as bf16 rows 463), 32 of up to 8 nodes x 64 heads
-// over up to 2048 60 us (8-bit; bf16 46), one of 16 x 16 over 4096 16.8 us.
+// measured burst rate, where the masks cost nothing that shows (the same products
+// without them, by stretches: 1720); 4 ragged ones of up to 61 nodes x 128 heads over
+// up to 32,768 8-bit positions 633 us (0.54: every row tile widens its keys again,
+// shared-memory bandwidth, below; the same rows in bf16 463), 32 of up to 8 nodes x 64
+// heads over up to 2048 60 us (8-bit; bf16 46: nearly every row tile is cut and
+// merged), one of 16 x 16 over 4096 17 us.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -98,6 +99,13 @@ constexpr int kMaxPairs = 80;
 // pairs are then in the same request or two, whose rows stay in L2, where
 // stretches of the line would have them in all requests at once (16 trees of 64
 // nodes x 128 heads over 8192, 151 MB of rows: 1740 us by stretches, 1510 so).
+// From 64 key tiles a pair on. bf16 rows, stretches / rounds, us, by tiles a pair:
+//   27   2 x 64 nodes x 128 heads over 4096   108 / 110
+//   54   4 x 64 over 4096   208 / 212;   8 x 64 over 2048   214 / 220
+//   108  4 x 64 over 8192   395 / 397;   16 x 32 over 4096   429 / 405
+//   216  8 x 64 over 8192   842 / 773;   64 x 16 over 4096   1098 / 806
+//        1 x 256 over 16,384   751 / 758 (a single request's rows are shared anyway)
+// Up to 64 requests, as many as the scratch below has room for.
 // 8-bit rows, whose kernel is bound by shared memory, gain nothing (4 trees of up to
 // 61 x 128 over up to 32,768: 635 and 631; 1 x 1024 x 128 over 8192: 2100 and 2135, the
 // walk's registers): they are shared out alike so that their results stay those of
@@ -1286,9 +1294,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Arg
 // cost more than the sums. The rows of all heads form one line that the grid's
 // warps share, four warps a row, each a quarter of its columns: every warp reads
 // all segments' records, at once, finds its row, and has the first eight parts'
-// sums on their way with their statistics. 16 nodes x 16 heads over 4096: 20.2 us
-// with the kernel above, 17.0 with this; one token x 16 heads: 16.5 and 14.5; but 32
-// tokens x 128 heads (a warp a row then): 101.4 and 102.2.
+// sums on their way with their statistics. Over 4096 positions, us with the kernel
+// above / this one: 16 rows 16.4 / 14.7, 256 rows 19.9 / 17.1, 512 rows 21.5 / 17.7,
+// 1024 rows 24.4 / 22.3, 2048 rows 29.3 / 29.8. Taken as long as the grid has a warp
+// for every quarter of a row, 608 rows.
 constexpr int kFewBlocks = 2;  // an SM
 constexpr int kRecords = (kMaxPairs + 31) / 32;  // a lane's
 __global__ void __launch_bounds__(32 * kMergeWarps, kFewBlocks)
@@ -1521,7 +1530,7 @@ ts_status attend(const void* q, int64_t q_stride, const int32_t* cu_q, int T, in
               : launch_chunk<DSA_CACHE_E4M3, false>(maps, a, stream);
   }
   if (st != TS_OK) return st;
-  // (a row for every four warps of its grid)
+  // (four warps of its grid for every row)
   const int blocks = kFewBlocks * sm_count();
   if (int64_t(T) * H * 4 <= int64_t(blocks) * kMergeWarps)
     return launch_after(chunk_merge_few_kernel, blocks, 32 * kMergeWarps, stream, a);

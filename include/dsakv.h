@@ -763,9 +763,9 @@ ts_status dsa_tree_plan(const int32_t* parent, const int32_t* cu_q, int T, int B
  *                                   (>= H * 576, a multiple of 8; 16-byte aligned)
  * The angle is reduced in whole 2^-64 turns: for |freq| <= 1 it is off by at
  * most |pos| 2^-54 of a turn, and then by its rounding to fp32, 2^-24 of its size
- * (at most half a turn). Sine and cosine are fp32, the values round once to bf16. A row whose slot is negative, or past
- * the cache (TS_DEVERR_SLOT_RANGE), is skipped; its queries are turned all the
- * same. H <= 1024. n = 0 enqueues nothing. */
+ * (at most half a turn). Sine and cosine are fp32, the values round once to bf16.
+ * A row whose slot is negative, or past the cache (TS_DEVERR_SLOT_RANGE), is
+ * skipped; its queries are turned all the same. H <= 1024. n = 0 enqueues nothing. */
 ts_status dsa_cache_append(const void* latent, int64_t latent_stride, const void* rope,
                            int64_t rope_stride, const int32_t* pos, const int32_t* slots, int n,
                            const double* freq, int pairs, void* cache, int64_t num_slots, int fmt,
@@ -846,7 +846,9 @@ ts_status dsa_cache_keep(void* cache, int64_t num_slots, int fmt, const int32_t*
  * A continuation of score -infinity (a logit of -infinity, a beam that is none)
  * is never chosen; where fewer than n are left, the last places have token and
  * parent -1 and score -infinity. A finished sequence is carried on by a row
- * that is -infinity but for its padding token. A NaN or +infinity among the
+ * that is -infinity but for its padding token. Tokens are masked by -infinity: a
+ * row that a finite value fills (hundreds of values equal to the best n in a few
+ * thousand tokens) takes up to a hundred times as long. A NaN or +infinity among the
  * logits or in cum sets TS_DEVERR_NAN and counts as -infinity. Scores are
  * compared in 64 bits. A log of a sum is off by less than 2^-17 (exponentials of
  * 2^-22 and at most 71 additions in fp32, the parts then joined in 64 bits; of
